@@ -45,6 +45,8 @@
  *   - WQ_ERR_CUDA reports a launch error (the CUDA error is left for
  *     cudaGetLastError to read);
  *   - W must be finite (not checked).
+ * The 8-bit integer calls (wq_quantize_i8, wq_gemm_i8, wq_gated_i8) state their
+ * own rules on strides, alignment and K.
  */
 #ifndef WQ_H
 #define WQ_H
@@ -66,7 +68,9 @@ typedef enum {
   WQ_ERR_UNSUPPORTED_DEVICE = 6,  /* current device is not compute capability 10.0 */
   WQ_ERR_CUDA = 7,                /* a CUDA runtime call or launch failed */
   WQ_ERR_DEVICE_TIMEOUT = 8,      /* a bounded device-side wait expired (see below) */
-  WQ_ERR_WORKSPACE = 9            /* workspace NULL or smaller than the call needs */
+  WQ_ERR_WORKSPACE = 9,           /* workspace NULL or smaller than the call needs */
+  WQ_ERR_TYPE = 10,               /* unknown wq_type or wq_act */
+  WQ_ERR_STRIDE = 11              /* a row stride too short, or a code matrix's not a multiple of 16 */
 } wq_status;
 
 /*
@@ -241,6 +245,77 @@ size_t wq_gemm_grouped_workspace_size(const wq_linear* linears, int count, int64
  *     Order them on one stream.
  */
 wq_status wq_gemm_grouped_noalloc(const wq_linear* linears, int count, int64_t M, int bits, void* stream);
+
+/*
+ * ---- 8-bit integer linears -------------------------------------------------
+ * Both sides of the product are 8-bit integers: activations with one scale for
+ * each token, taken at run time, weights with one scale for each output
+ * channel ("Platform For AI: BladeLLM model quantization", the act-and-weight
+ * mode: dynamic per-token activations, per-channel weights, INT8).
+ *
+ * Rules common to the three calls, beside those above:
+ *   - matrices are row-major with a row stride (ldx, ldw, ...) in elements, at
+ *     least the row's length and below 2^31; what lies between rows is neither
+ *     read into a result nor written;
+ *   - int8 code matrices start 16-byte aligned and their strides are multiples
+ *     of 16; other pointers need the alignment of their element type only;
+ *   - 1 <= K <= 131071 (a sum of K products of 8-bit codes fits int32); any K,
+ *     no multiple is needed;
+ *   - outputs must not overlap inputs.
+ */
+typedef enum { WQ_TYPE_BF16 = 0, WQ_TYPE_F16 = 1, WQ_TYPE_F32 = 2 } wq_type;
+typedef enum {
+  WQ_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+  WQ_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+  WQ_ACT_GELU_TANH = 2  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} wq_act;
+
+/*
+ * wq_quantize_i8 -- every row of x to 8-bit codes with a scale of its own.
+ *
+ *   s = max_k |x_k| * fp32(1/127) in fp32,  q_k = rint(x_k / s)  (of the exact
+ *   quotient, half to even, kept within -127..127); s = 0 and q = 0 for a row of zeros;
+ *   s = NaN and q = 0 for a row that holds an infinity or a NaN, so that
+ *   every product with that row is NaN
+ *
+ *   x        in   x_type [R, K], row stride ldx: tokens, or rows of weights
+ *   codes    out  int8 [R, K], row stride ldc (16-byte aligned, ldc % 16 == 0)
+ *   scales   out  fp32 [R]
+ *
+ * Codes and scales are bit-exact by that definition.
+ */
+wq_status wq_quantize_i8(const void* x, wq_type x_type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
+                         int64_t ldc, float* scales, void* stream);
+
+/*
+ * wq_gemm_i8 -- y[m, n] = x_scales[m] w_scales[n] sum_k x[m, k] w[n, k].
+ *
+ *   x         in   int8 [M, K], row stride ldx; x_scales fp32 [M]
+ *   w         in   int8 [N, K], row stride ldw; w_scales fp32 [N]
+ *   y         out  y_type [M, N], row stride ldy
+ *
+ * The sum is exact (int32); it is converted to fp32, multiplied by x_scales[m],
+ * then by w_scales[n] (three fp32 roundings) and rounded once to y_type.  So y
+ * does not depend on M, on the other rows or on which kernel ran, bit for bit.
+ * A non-finite scale gives a non-finite row or column.
+ */
+wq_status wq_gemm_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_t M, int64_t N, int64_t K,
+                     const int8_t* w, int64_t ldw, const float* w_scales, void* y, wq_type y_type, int64_t ldy,
+                     void* stream);
+
+/*
+ * wq_gated_i8 -- the first half of a gated feed-forward block in one kernel:
+ * h = act(g) * u, with g and u the products of x with the gate's and the up
+ * projection's weights, each as in wq_gemm_i8, kept in fp32 up to the one
+ * rounding of h to h_type.
+ *
+ *   w_gate, w_up   in   int8 [N, K], both with row stride ldw; scales fp32 [N]
+ *   act                 the gate's activation
+ *   h              out  h_type [M, N], row stride ldh
+ */
+wq_status wq_gated_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_t M, int64_t N, int64_t K,
+                      const int8_t* w_gate, const float* gate_scales, const int8_t* w_up, const float* up_scales,
+                      int64_t ldw, wq_act act, void* h, wq_type h_type, int64_t ldh, void* stream);
 
 /* Number of uint32 words of packed codes for an [N, K] matrix: N*K*bits/32
  * (0 if bits or K are invalid). */

@@ -9,6 +9,12 @@ be loaded, importing this package fails.
     codes, scales, zeros = wq_quantize_rtn(W_f16, bits, group)
     y = wq_gemm(x_bf16, codes, scales, zeros, bits, group, N, K)
     ys = wq_gemm_grouped([(x, codes, scales, zeros, N, K, group), ...], bits, workspace)
+
+8-bit integers on both sides (one scale per token, one per output channel):
+
+    q, qs = wq_quantize_i8(x)                       # tokens, or rows of weights
+    y = wq_gemm_i8(q, qs, w, ws)
+    h = wq_gated_i8(q, qs, w_gate, gate_scales, w_up, up_scales, act="silu")
 """
 from __future__ import annotations
 
@@ -31,10 +37,12 @@ WQ_ERR_UNSUPPORTED_DEVICE = 6
 WQ_ERR_CUDA = 7
 WQ_ERR_DEVICE_TIMEOUT = 8
 WQ_ERR_WORKSPACE = 9
+WQ_ERR_TYPE = 10
+WQ_ERR_STRIDE = 11
 
 # Functions the header declares (the tests check the library exports them).
 EXPORTED = ("wq_quantize_rtn", "wq_quantize_rtn_sym", "wq_gemm", "wq_gemm_grouped", "wq_gemm_grouped_workspace_size",
-            "wq_gemm_grouped_noalloc",
+            "wq_gemm_grouped_noalloc", "wq_quantize_i8", "wq_gemm_i8", "wq_gated_i8",
             "wq_codes_words", "wq_params_count", "wq_status_string", "wq_last_device_error")
 
 
@@ -65,6 +73,12 @@ def _load():
     lib.wq_gemm_grouped_noalloc.restype = ci
     lib.wq_gemm_grouped_workspace_size.argtypes = [lp, ci, i64, ci]
     lib.wq_gemm_grouped_workspace_size.restype = ctypes.c_size_t
+    lib.wq_quantize_i8.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, vp]
+    lib.wq_quantize_i8.restype = ci
+    lib.wq_gemm_i8.argtypes = [vp, i64, vp, i64, i64, i64, vp, i64, vp, vp, ci, i64, vp]
+    lib.wq_gemm_i8.restype = ci
+    lib.wq_gated_i8.argtypes = [vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64, ci, vp, ci, i64, vp]
+    lib.wq_gated_i8.restype = ci
     lib.wq_codes_words.argtypes = [i64, i64, ci]
     lib.wq_codes_words.restype = ctypes.c_size_t
     lib.wq_params_count.argtypes = [i64, i64, i64]
@@ -242,3 +256,124 @@ def wq_gemm_grouped_noalloc(items, bits: int, stream=None):
     st = lib.wq_gemm_grouped_noalloc(arr, len(items), M, bits, _stream_ptr(stream))
     _check(st, "wq_gemm_grouped_noalloc")
     return ys
+
+
+# ---- 8-bit integers on both sides -------------------------------------------
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # wq_type
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}                        # wq_act
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    """Row stride of a 2-D CUDA tensor whose columns are adjacent."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have adjacent columns (stride 1)")
+    # the stride of a single row is never taken: any valid one will do
+    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _codes(t: torch.Tensor, what: str) -> int:
+    if t.dtype != torch.int8:
+        raise ValueError(f"{what} must be int8 codes")
+    return _rows(t, what)
+
+
+def _scales(t: torch.Tensor, n: int, dev, what: str) -> int:
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 [{n}] tensor on the codes' device")
+    return t.data_ptr()
+
+
+def _call(fn, where: str, dev, stream, *args) -> None:
+    """fn(*args, stream) with `dev` current: its current stream when `stream` is None."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    if st != WQ_OK:
+        raise WQError(st, where)
+
+
+def _output(y, M: int, N: int, dtype, dev, what: str):
+    if y is None:
+        if dtype not in _TYPES:
+            raise ValueError("dtype must be torch.bfloat16, torch.float16 or torch.float32")
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+        return y, N
+    if y.dtype not in _TYPES or tuple(y.shape) != (M, N) or y.device != dev:
+        raise ValueError(f"{what} must be a bf16, fp16 or fp32 [{M}, {N}] tensor on the codes' device")
+    ld = _rows(y, what)
+    return y, ld if M > 1 else max(ld, N)
+
+
+def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """Quantise every row of bf16/fp16/fp32 ``x`` [R, K] (CUDA, any row stride)
+    -> (int8 codes [R, K], fp32 scales [R]), ``x ~ codes * scales[:, None]``.
+    The codes' rows start at multiples of 16 bytes: for other K the returned
+    tensor is a view of a wider one."""
+    if x.dtype not in _TYPES:
+        raise ValueError("x must be bf16, fp16 or fp32")
+    ldx = _rows(x, "x")
+    R, K = x.shape
+    dev = x.device
+    if codes is None:
+        ldc = (K + 15) // 16 * 16
+        codes = torch.empty((R, ldc), dtype=torch.int8, device=dev)
+        if ldc != K:
+            codes = codes[:, :K]
+    else:
+        ldc = _codes(codes, "codes")
+        if codes.shape != x.shape or codes.device != dev:
+            raise ValueError("codes must have x's shape and device")
+    if scales is None:
+        scales = torch.empty((R,), dtype=torch.float32, device=dev)
+        sp = scales.data_ptr()
+    else:
+        sp = _scales(scales, R, dev, "scales")
+    _call(lib.wq_quantize_i8, "wq_quantize_i8", dev, stream, x.data_ptr(), _TYPES[x.dtype], R, K, ldx,
+          codes.data_ptr(), ldc, sp)
+    return codes, scales
+
+
+def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y=None,
+               dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """``y[m, n] = x_scales[m] * w_scales[n] * sum_k x[m, k] w[n, k]`` for int8
+    codes ``x`` [M, K] and ``w`` [N, K] -> ``y`` [M, N] of ``dtype`` (or the
+    given ``y``'s type).  Row strides of codes are multiples of 16."""
+    ldx, ldw = _codes(x, "x"), _codes(w, "w")
+    M, K = x.shape
+    N, Kw = w.shape
+    dev = x.device
+    if Kw != K or w.device != dev:
+        raise ValueError("w must be [N, K] with x's K, on x's device")
+    xs, ws = _scales(x_scales, M, dev, "x_scales"), _scales(w_scales, N, dev, "w_scales")
+    y, ldy = _output(y, M, N, dtype, dev, "y")
+    _call(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w.data_ptr(), ldw, ws,
+          y.data_ptr(), _TYPES[y.dtype], ldy)
+    return y
+
+
+def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, gate_scales: torch.Tensor,
+                w_up: torch.Tensor, up_scales: torch.Tensor, act: str = "silu", h=None, dtype=torch.bfloat16,
+                stream=None) -> torch.Tensor:
+    """``h = act(x . w_gate^T) * (x . w_up^T)`` on int8 codes, both products
+    scaled as in ``wq_gemm_i8``, in one kernel; ``act``: "silu", "gelu" (erf)
+    or "gelu_tanh"."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    ldx, ldw, ldu = _codes(x, "x"), _codes(w_gate, "w_gate"), _codes(w_up, "w_up")
+    M, K = x.shape
+    N, Kw = w_gate.shape
+    dev = x.device
+    if Kw != K or w_gate.device != dev or w_up.shape != w_gate.shape or w_up.device != dev or ldu != ldw:
+        raise ValueError("w_gate and w_up must be [N, K] with x's K and one row stride, on x's device")
+    xs = _scales(x_scales, M, dev, "x_scales")
+    gs, us = _scales(gate_scales, N, dev, "gate_scales"), _scales(up_scales, N, dev, "up_scales")
+    h, ldh = _output(h, M, N, dtype, dev, "h")
+    _call(lib.wq_gated_i8, "wq_gated_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w_gate.data_ptr(), gs,
+          w_up.data_ptr(), us, ldw, _ACTS[act], h.data_ptr(), _TYPES[h.dtype], ldh)
+    return h

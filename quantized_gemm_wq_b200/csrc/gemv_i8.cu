@@ -1,0 +1,161 @@
+// gemv_i8.cu -- 8-bit integer linears for few tokens, on warp-level MMAs.
+//
+// With a handful of tokens the product is bound by the read of the weights, a
+// byte each.  The weight rows are the M side of mma.sync.m16n8k32 (s8 x s8 ->
+// s32), the tokens its N side, so up to 8 tokens cost one MMA per 512 weights.
+// A sum over k may be taken in any order, so both operands are loaded 16 bytes
+// a lane from the same places of their rows and the MMA's k index is renamed:
+// lane (g, t) holds bytes 16 t .. 16 t + 15 of a 64-byte chunk of rows g and
+// g + 8 and of token g, which are the A and B fragments of two MMAs.  Weights
+// go straight from memory to registers; nothing is staged.
+//
+// One CTA computes 16 output rows (of both projections in a gated call) for
+// its block of tokens; its warps take the 64-byte chunks of K in turn and
+// their int32 sums meet in shared memory.
+#include "i8.cuh"
+#include "wq_internal.cuh"
+
+namespace wq {
+namespace i8 {
+namespace {
+
+constexpr int kMaxWarps = 16;
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Weights are read once: past L1.
+__device__ __forceinline__ uint4 ld_stream(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// The first `valid` (< 16) bytes at p, zeros behind them.
+__device__ __forceinline__ uint4 ld_part(const int8_t* p, int valid) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < valid) w[i >> 2] |= uint32_t(uint8_t(p[i])) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// NT: blocks of 8 tokens; RT: tiles of 16 rows (gated: the gate's and the up
+// projection's); U: chunks in flight per warp.
+template <int NT, bool GATED, int U>
+__global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L) {
+  constexpr int RT = GATED ? 2 : 1;
+  extern __shared__ int red[];   // [warp][RT][NT * 8 tokens][16 rows]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * (8 * NT);
+
+  const int8_t* wp[RT][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t n = min(n0 + g + 8 * h, L.N - 1);   // rows past the last read it again; nothing is stored for them
+    wp[0][h] = L.w0 + n * L.ldw + 16 * t;
+    if constexpr (GATED) wp[1][h] = L.w1 + n * L.ldw + 16 * t;
+  }
+  const int8_t* xp[NT];
+  bool xlive[NT];
+#pragma unroll
+  for (int b = 0; b < NT; ++b) {
+    const int64_t m = m0 + 8 * b + g;
+    xlive[b] = m < L.M;
+    xp[b] = L.x + (xlive[b] ? m : 0) * L.ldx + 16 * t;
+  }
+  int acc[RT][NT][4] = {};
+  auto feed = [&](const uint4 (&a)[RT][2], const uint4 (&x)[NT]) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) {
+        mma_s8(acc[r][b], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y, x[b].x, x[b].y);
+        mma_s8(acc[r][b], a[r][0].z, a[r][1].z, a[r][0].w, a[r][1].w, x[b].z, x[b].w);
+      }
+  };
+
+  const int64_t chunks = L.K / 64;
+  int64_t c = warp;
+  for (; c + int64_t(U - 1) * warps < chunks; c += int64_t(U) * warps) {
+    uint4 a[U][RT][2], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (c + int64_t(u) * warps) * 64;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[u][r][h] = ld_stream(wp[r][h] + k);
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+        x[u][b] = xlive[b] ? __ldg(reinterpret_cast<const uint4*>(xp[b] + k)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) feed(a[u], x[u]);
+  }
+  for (; c * 64 < L.K; c += warps) {   // fewer than U chunks left; the last one may be short
+    const int64_t k = c * 64;
+    const int valid = int(min(int64_t(16), L.K - k - 16 * t));
+    uint4 a[RT][2], x[NT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) a[r][h] = valid >= 16 ? ld_stream(wp[r][h] + k) : ld_part(wp[r][h] + k, valid);
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+      x[b] = !xlive[b]     ? make_uint4(0, 0, 0, 0)
+             : valid >= 16 ? __ldg(reinterpret_cast<const uint4*>(xp[b] + k))
+                           : ld_part(xp[b] + k, valid);
+    feed(a, x);
+  }
+
+  constexpr int kTok = 8 * NT;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[((warp * RT + r) * kTok + 8 * b + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[r][b][i];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kTok * 16; o += blockDim.x) {
+    const int64_t n = n0 + (o & 15), m = m0 + (o >> 4);
+    if (n >= L.N || m >= L.M) continue;
+    int s[RT] = {};
+    for (int w = 0; w < warps; ++w)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s[r] += red[(w * RT + r) * kTok * 16 + o];
+    const float sx = L.xs[m];
+    float v = scaled(s[0], sx, L.s0[n]);
+    if constexpr (GATED) v = apply_act(v, L.act) * scaled(s[1], sx, L.s1[n]);
+    store_one(L.y, m * L.ldy + n, v, L.type);
+  }
+}
+
+template <int NT, bool GATED, int U>
+cudaError_t launch_nt(const Linear& L, cudaStream_t st) {
+  const int64_t gx = (L.N + 15) / 16, gy = (L.M + 8 * NT - 1) / (8 * NT);
+  if (gx > 0x7fffffff || gy > 65535) return cudaErrorInvalidValue;
+  const int warps = 8;
+  const size_t smem = size_t(warps) * (GATED ? 2 : 1) * NT * 8 * 16 * 4;
+  gemv_i8_kernel<NT, GATED, U><<<dim3(unsigned(gx), unsigned(gy)), 32 * warps, smem, st>>>(L);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemv(const Linear& L, cudaStream_t st) {
+  const bool gated = L.act != kNone;
+  if (L.M <= 8) return gated ? launch_nt<1, true, 4>(L, st) : launch_nt<1, false, 4>(L, st);
+  return gated ? launch_nt<2, true, 2>(L, st) : launch_nt<2, false, 4>(L, st);
+}
+
+}  // namespace i8
+}  // namespace wq

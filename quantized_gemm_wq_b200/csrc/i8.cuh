@@ -1,0 +1,73 @@
+// i8.cuh -- what the kernels of the 8-bit integer linears share: the argument
+// block, the activations, the output conversion.
+//
+//   y[m, n] = s_x[m] s_w[n] sum_k q_x[m, k] q_w[n, k]
+//   h[m, n] = act(g[m, n]) u[m, n],  g and u as y with the gate's and the up
+//             projection's weights
+//
+// The sum is exact in int32 (the C ABI refuses K whose sums could pass 2^31),
+// so neither the order of the terms nor a split of K over warps, CTAs or
+// clusters changes a result: y is bit for bit the same from every kernel.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace wq {
+namespace i8 {
+
+enum Type { kBF16 = 0, kF16 = 1, kF32 = 2 };                  // wq_type
+enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2, kNone = -1 };  // wq_act; kNone: no gate
+
+inline int type_bytes(int t) { return t == kF32 ? 4 : 2; }
+
+// One product, or the two of a gated call: w0 / s0 the weights (the gate's),
+// w1 / s1 the up projection's.  Row strides in elements.
+struct Linear {
+  const int8_t* x;
+  const float* xs;
+  const int8_t* w0;
+  const float* s0;
+  const int8_t* w1;
+  const float* s1;
+  void* y;
+  int64_t M, N, K, ldx, ldw, ldy;
+  int type;   // of y
+  int act;    // kNone: y is the product
+};
+
+// act(g).  Forms without cancellation: for g << 0 the result keeps its
+// relative accuracy (1 + erf would lose it), for g << 0 in silu the division
+// by an overflowed exponential gives -0, the limit.
+__device__ __forceinline__ float apply_act(float g, int act) {
+  if (act == kSilu) return g / (1.0f + expf(-g));
+  if (act == kGelu) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  // g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)) = 0.5 g (1 + tanh(...))
+  const float t = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+  return g / (1.0f + expf(-t));
+}
+
+// acc s_x s_w, scaled in that order: s_x s_w alone could leave fp32's range
+// where the result does not.  acc above 2^24 is rounded to fp32 (half a step,
+// 2^-24), as each of the two products is.
+__device__ __forceinline__ float scaled(int acc, float sx, float sw) { return float(acc) * sx * sw; }
+
+__device__ __forceinline__ void store_one(void* y, int64_t i, float v, int type) {
+  if (type == kBF16)
+    static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
+  else if (type == kF16)
+    static_cast<__half*>(y)[i] = __float2half_rn(v);
+  else
+    static_cast<float*>(y)[i] = v;
+}
+
+cudaError_t launch_quantize(const void* x, int type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
+                            int64_t ldc, float* scales, cudaStream_t st);
+cudaError_t launch_gemv(const Linear& L, cudaStream_t st);
+
+// One call's kernel (arguments already checked by the C ABI).
+inline cudaError_t launch_linear(const Linear& L, cudaStream_t st) { return launch_gemv(L, st); }
+
+}  // namespace i8
+}  // namespace wq

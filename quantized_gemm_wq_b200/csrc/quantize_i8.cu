@@ -1,0 +1,238 @@
+// quantize_i8.cu -- rows to 8-bit integers with one scale a row.
+//
+// ("Platform For AI: BladeLLM model quantization", the act-and-weight mode:
+// per-token dynamic scales for activations, per-channel scales for weights,
+// INT8.)  For a row x of K values
+//
+//   s = max |x| fp32(1 / 127),   q = clamp(rint(x / s), -127, 127),  0 where s = 0
+//
+// with rint of the exact quotient, half to even; a row that holds an infinity
+// or a NaN gets s = NaN and q = 0, so that every product with it is NaN.
+//
+// Bound by memory: one read of x, one write of a byte an element.  A row is
+// read once and stays in registers (as loaded) between its maximum and its
+// codes; only rows too long for that are read a second time.
+//
+// The maximum is taken over the magnitude bits as unsigned integers: they
+// order as the values do, with infinities and then NaNs on top, so one integer
+// maximum finds the scale and the non-finite rows, two 16-bit values at a time.
+//
+// The codes are exact without a division per element.  With c = fp32(1/s) the
+// product x c is within 127.5 * 2^-24 < 2^-17 of x/s; t = fma(x, c, 1.5 2^23)
+// rounds it to the nearest integer n (the code is t's low byte) and d =
+// fma(x, c, -n) is its distance from there.  Where |d| <= 1/2 - 2^-14 the
+// exact quotient rounds to the same n.  Else, about one element in ten
+// thousand, the quotient is taken in 64 bits: quotients of two 24-bit numbers
+// that are not half-integers differ from one by over 2^-33 of their size, far
+// above its 2^-53, so its rounding is the exact one's.  Scales under 2^-100,
+// where 1/s or the error bound would leave the normal range, take the 64-bit
+// quotient for every element.
+#include <type_traits>
+
+#include "i8.cuh"
+#include "wq_internal.cuh"
+
+namespace wq {
+namespace i8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// VE consecutive elements of a row as loaded: 16 bytes.
+template <int TYPE>
+struct Vec {
+  static constexpr int VE = TYPE == kF32 ? 4 : 8;
+  using Elem = typename std::conditional<TYPE == kF32, uint32_t, uint16_t>::type;
+
+  // The magnitude bits' maximum as fp32 bits, folded into m (in the type's own bits).
+  static __device__ __forceinline__ uint32_t fold(uint32_t m, const uint4& v) {
+    if constexpr (TYPE == kF32) {
+      m = max(m, max(v.x & 0x7fffffffu, v.y & 0x7fffffffu));
+      return max(m, max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+    } else {
+      m = __vmaxu2(m, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+      return __vmaxu2(m, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    }
+  }
+  // The folded maximum (over lanes too) as the bits of an fp32 number.
+  static __device__ __forceinline__ uint32_t to_f32_bits(uint32_t m) {
+    if constexpr (TYPE == kF32) return m;
+    m = max(m & 0xffffu, m >> 16);
+    if constexpr (TYPE == kBF16) return m << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(uint16_t(m))));
+  }
+  static __device__ __forceinline__ float value(const uint4& v, int i) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (TYPE == kF32) return __uint_as_float(w[i]);
+    const uint32_t h = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+    if constexpr (TYPE == kBF16) return __uint_as_float(h << 16);
+    return __half2float(__ushort_as_half(uint16_t(h)));
+  }
+};
+
+// VE elements from k on; elements outside 0 .. K - 1 read as 0.
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ uint4 load_vec(const typename Vec<TYPE>::Elem* row, int64_t k, int64_t K) {
+  constexpr int VE = Vec<TYPE>::VE;
+  if (k + VE <= K && (ALIGNED || k >= 0)) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < VE; ++i)
+    if (k + i >= 0 && k + i < K) {
+      const uint32_t e = row[k + i];
+      if constexpr (TYPE == kF32) w[i] = e;
+      else w[i >> 1] |= e << (16 * (i & 1));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int exact_code(float x, float s) {
+  return int(rint(fmin(fmax(double(x) / double(s), -127.0), 127.0)));
+}
+
+// Codes of the elements of v, one byte each, first element lowest.
+template <int TYPE>
+__device__ __forceinline__ void codes_of(const uint4& v, float s, float inv, uint32_t (&out)[2]) {
+  constexpr int VE = Vec<TYPE>::VE;
+  uint32_t b[VE];
+  float worst = 0.0f;
+  if (inv != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float x = Vec<TYPE>::value(v, i);
+      const float t = __fmaf_rn(x, inv, 12582912.0f);   // 1.5 2^23: the unit in the last place is 1
+      b[i] = __float_as_uint(t);
+      worst = fmaxf(worst, fabsf(__fmaf_rn(x, inv, -(t - 12582912.0f))));
+    }
+  } else {
+    worst = 1.0f;
+  }
+  if (worst > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) b[i] = uint32_t(exact_code(Vec<TYPE>::value(v, i), s));
+  }
+#pragma unroll
+  for (int i = 0; i < VE; i += 4)
+    out[i / 4] = __byte_perm(__byte_perm(b[i], b[i + 1], 0x0040), __byte_perm(b[i + 2], b[i + 3], 0x0040), 0x5410);
+}
+
+// `wpr` warps per row, kThreads / 32 / wpr rows per CTA.  NV > 0: each thread
+// holds its NV vectors of the row in registers; NV = 0: two passes over memory.
+template <int TYPE, int NV, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) quantize_i8_kernel(const void* __restrict__ xv, int64_t R, int64_t K,
+                                                               int64_t ldx, int8_t* __restrict__ codes, int64_t ldc,
+                                                               float* __restrict__ scales, int wpr) {
+  using V = Vec<TYPE>;
+  constexpr int VE = V::VE;
+  __shared__ uint32_t smax[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r = int64_t(blockIdx.x) * (kThreads / 32 / wpr) + warp / wpr;
+  const bool live = r < R;
+  const int t0 = (warp % wpr) * 32 + lane, tn = 32 * wpr;
+  const auto* row = static_cast<const typename V::Elem*>(xv) + (live ? r * ldx : 0);
+  // elements between the 16-byte boundary at or below the row's start and the
+  // row: vector j holds elements j VE - off ..
+  const int off = ALIGNED ? 0 : int((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(typename V::Elem));
+  const int64_t nvec = live ? (K + off + VE - 1) / VE : 0;
+
+  uint4 v[NV > 0 ? NV : 1];
+  uint32_t m = 0;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t j = t0 + int64_t(i) * tn;
+      v[i] = j < nvec ? load_vec<TYPE, ALIGNED>(row, j * VE - off, K) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = V::fold(m, v[i]);
+  } else {
+#pragma unroll 4
+    for (int64_t j = t0; j < nvec; j += tn) m = V::fold(m, load_vec<TYPE, ALIGNED>(row, j * VE - off, K));
+  }
+  m = V::to_f32_bits(m);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (wpr > 1) {
+    if (lane == 0) smax[warp] = m;
+    __syncthreads();
+    const int w0 = warp / wpr * wpr;
+    m = 0;
+    for (int w = 0; w < wpr; ++w) m = max(m, smax[w0 + w]);
+  }
+  if (!live) return;
+  const float s = __uint_as_float(m) * (1.0f / 127.0f);
+  const bool finite = m < 0x7f800000u;
+  if (t0 == 0) scales[r] = finite ? s : __uint_as_float(0x7fc00000u);
+  const bool zero = !finite || s == 0.0f;
+  const float inv = s >= 0x1p-100f && finite ? __fdiv_rn(1.0f, s) : 0.0f;
+  int8_t* out = codes + r * ldc;
+  auto put = [&](int64_t j, const uint4& x) {
+    uint32_t c[2] = {0u, 0u};
+    if (!zero) codes_of<TYPE>(x, s, inv, c);
+    const int64_t k = j * VE - off;
+    if (ALIGNED && k + VE <= K) {
+      if constexpr (VE == 8) *reinterpret_cast<uint2*>(out + k) = make_uint2(c[0], c[1]);
+      else *reinterpret_cast<uint32_t*>(out + k) = c[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i)
+        if (k + i >= 0 && k + i < K) out[k + i] = int8_t(c[i / 4] >> (8 * (i & 3)));
+    }
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t j = t0 + int64_t(i) * tn;
+      if (j < nvec) put(j, v[i]);
+    }
+  } else {
+#pragma unroll 2
+    for (int64_t j = t0; j < nvec; j += tn) put(j, load_vec<TYPE, ALIGNED>(row, j * VE - off, K));
+  }
+}
+
+template <int TYPE, bool ALIGNED>
+cudaError_t launch_typed(const void* x, int64_t R, int64_t K, int64_t ldx, int8_t* codes, int64_t ldc, float* scales,
+                         cudaStream_t st) {
+  constexpr int VE = Vec<TYPE>::VE;
+  const int64_t nvec = (K + (ALIGNED ? 0 : VE - 1) + VE - 1) / VE;   // the most that a row can span
+  // warps per row: two vectors a thread and more before the next warp joins
+  // in, and all eight when there are few rows
+  int wpr = 1;
+  while (wpr < 8 && (nvec > 64 * wpr || (R < 1024 && nvec > 32 * wpr))) wpr *= 2;
+  const int64_t per = (nvec + 32 * wpr - 1) / (32 * wpr);
+  const int64_t grid = (R + 8 / wpr - 1) / (8 / wpr);
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 g{unsigned(grid)}, b{kThreads};
+  if (per <= 1)
+    quantize_i8_kernel<TYPE, 1, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
+  else if (per <= 2)
+    quantize_i8_kernel<TYPE, 2, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
+  else if (per <= 4)
+    quantize_i8_kernel<TYPE, 4, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
+  else if (per <= 8)
+    quantize_i8_kernel<TYPE, 8, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
+  else
+    quantize_i8_kernel<TYPE, 0, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
+  return cudaGetLastError();
+}
+
+template <int TYPE>
+cudaError_t launch_aligned(const void* x, int64_t R, int64_t K, int64_t ldx, int8_t* codes, int64_t ldc,
+                           float* scales, cudaStream_t st) {
+  const int64_t row_bytes = ldx * int64_t(type_bytes(TYPE));
+  if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (R == 1 || row_bytes % 16 == 0))
+    return launch_typed<TYPE, true>(x, R, K, ldx, codes, ldc, scales, st);
+  return launch_typed<TYPE, false>(x, R, K, ldx, codes, ldc, scales, st);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const void* x, int type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
+                            int64_t ldc, float* scales, cudaStream_t st) {
+  if (type == kBF16) return launch_aligned<kBF16>(x, R, K, ldx, codes, ldc, scales, st);
+  if (type == kF16) return launch_aligned<kF16>(x, R, K, ldx, codes, ldc, scales, st);
+  return launch_aligned<kF32>(x, R, K, ldx, codes, ldc, scales, st);
+}
+
+}  // namespace i8
+}  // namespace wq

@@ -7,6 +7,7 @@
 
 #include "../../include/wq.h"
 #include "grouped.h"
+#include "i8.cuh"
 #include "wq_internal.cuh"
 
 namespace {
@@ -122,6 +123,31 @@ std::vector<wq::GroupedLinear> grouped_fast_list(const wq_linear* lins, int coun
   return v;
 }
 
+// ---- 8-bit integer linears ----
+
+bool valid_type(int t) { return t == WQ_TYPE_BF16 || t == WQ_TYPE_F16 || t == WQ_TYPE_F32; }
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes)) == 0; }
+
+// Longest row: 2^14 K, the largest magnitude of a sum of K products of two
+// 8-bit codes, has to stay below 2^31.
+constexpr int64_t kMaxI8K = 131071;
+
+wq_status check_gemm_i8(const wq::i8::Linear& L) {
+  if (!L.x || !L.xs || !L.w0 || !L.s0 || !L.y) return WQ_ERR_NULL;
+  if (L.act != wq::i8::kNone && (!L.w1 || !L.s1)) return WQ_ERR_NULL;
+  if (!valid_type(L.type)) return WQ_ERR_TYPE;
+  if (L.act != wq::i8::kNone && L.act != WQ_ACT_SILU && L.act != WQ_ACT_GELU && L.act != WQ_ACT_GELU_TANH)
+    return WQ_ERR_TYPE;
+  if (L.M < 1 || L.N < 1 || L.K < 1 || L.M >= kMaxDim || L.N >= kMaxDim || L.K > kMaxI8K) return WQ_ERR_SHAPE;
+  if (L.ldx < L.K || L.ldw < L.K || L.ldy < L.N || L.ldx >= kMaxDim || L.ldw >= kMaxDim || L.ldy >= kMaxDim)
+    return WQ_ERR_STRIDE;
+  if (L.ldx % 16 != 0 || L.ldw % 16 != 0) return WQ_ERR_STRIDE;
+  if (!aligned16(L.x) || !aligned16(L.w0) || (L.w1 && !aligned16(L.w1)) || !aligned_to(L.xs, 4) ||
+      !aligned_to(L.s0, 4) || !aligned_to(L.s1, 4) || !aligned_to(L.y, wq::i8::type_bytes(L.type)))
+    return WQ_ERR_ALIGN;
+  return check_device();
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,6 +174,8 @@ const char* wq_status_string(wq_status s) {
     case WQ_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case WQ_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait expired";
     case WQ_ERR_WORKSPACE: return "the workspace is NULL or smaller than the call needs";
+    case WQ_ERR_TYPE: return "unknown element type or activation";
+    case WQ_ERR_STRIDE: return "a row stride is shorter than the row, or (8-bit codes) not a multiple of 16";
   }
   return "unknown status";
 }
@@ -279,6 +307,43 @@ wq_status wq_gemm_grouped_noalloc(const wq_linear* linears, int count, int64_t M
     e = dispatch_one(g.x, M, g.N, g.K, g.codes, g.scales, g.zeros, bits, g.group, g.y, strm);
   }
   return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+}
+
+wq_status wq_quantize_i8(const void* x, wq_type x_type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
+                         int64_t ldc, float* scales, void* stream) {
+  if (!x || !codes || !scales) return WQ_ERR_NULL;
+  if (!valid_type(x_type)) return WQ_ERR_TYPE;
+  if (R < 1 || K < 1 || R >= kMaxDim || K > kMaxI8K) return WQ_ERR_SHAPE;
+  if (ldx < K || ldc < K || ldx >= kMaxDim || ldc >= kMaxDim || ldc % 16 != 0) return WQ_ERR_STRIDE;
+  if (!aligned_to(x, wq::i8::type_bytes(x_type)) || !aligned16(codes) || !aligned_to(scales, 4)) return WQ_ERR_ALIGN;
+  const wq_status st = check_device();
+  if (st != WQ_OK) return st;
+  const cudaError_t e =
+      wq::i8::launch_quantize(x, x_type, R, K, ldx, codes, ldc, scales, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+}
+
+wq_status wq_gemm_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_t M, int64_t N, int64_t K,
+                     const int8_t* w, int64_t ldw, const float* w_scales, void* y, wq_type y_type, int64_t ldy,
+                     void* stream) {
+  const wq::i8::Linear L{x, x_scales, w,   w_scales, nullptr, nullptr,     y,
+                         M, N,        K,   ldx,      ldw,     ldy,         int(y_type),
+                         wq::i8::kNone};
+  const wq_status st = check_gemm_i8(L);
+  if (st != WQ_OK) return st;
+  return wq::i8::launch_linear(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
+}
+
+wq_status wq_gated_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_t M, int64_t N, int64_t K,
+                      const int8_t* w_gate, const float* gate_scales, const int8_t* w_up, const float* up_scales,
+                      int64_t ldw, wq_act act, void* h, wq_type h_type, int64_t ldh, void* stream) {
+  const wq::i8::Linear L{x, x_scales, w_gate, gate_scales, w_up, up_scales,   h,
+                         M, N,        K,      ldx,         ldw,  ldh,         int(h_type),
+                         int(act)};
+  if (L.act == wq::i8::kNone) return WQ_ERR_TYPE;
+  const wq_status st = check_gemm_i8(L);
+  if (st != WQ_OK) return st;
+  return wq::i8::launch_linear(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
 wq_status wq_last_device_error(void) {
