@@ -1,0 +1,662 @@
+// gemm_i8.cu -- 8-bit integer linears on the Blackwell tensor cores
+// (tcgen05.mma kind::i8, s8 x s8 -> s32, accumulators in tensor memory).
+//
+// Both operands are K-major bytes, so TMA brings them straight into the
+// 128-byte swizzled layout the MMA reads: 128 bytes of K a row and stage, four
+// MMAs of K = 32 each.  Bytes past K and rows past the matrices read as zero.
+// int32 sums are exact, so a split of K needs no order.
+//
+// split kernel (a batch of up to 256 tokens): bound by the read of the
+//   weights.  128 weight rows (gated: 64 of the gate and the same 64 of the up
+//   projection) are the MMA's M side, the tokens, padded to a multiple of 32,
+//   its N side: every weight byte is read once.  K is split over a cluster
+//   when the tiles alone leave SMs idle; each rank parks its int32 tile in its
+//   own shared memory and sums a share of the tokens over all ranks through
+//   distributed shared memory.
+// pair kernel (larger batches): bound by the tensor cores.  Two SMs work on one
+//   tile of 256 tokens x BN weight rows (cta_group::2): each loads its 128
+//   tokens and half of the weight rows (gated: one SM the gate's, the other
+//   the up projection's), so a byte of shared memory feeds twice the MMAs.
+//   Persistent, two accumulators: a tile's epilogue runs beside the next
+//   tile's MMAs.
+//
+// Every wait is bounded (bounded_wait.cuh): an expired wait raises this file's
+// device flag, the kernel drains its copies and MMAs, frees its tensor memory
+// and returns.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "i8.cuh"
+#include "wq_internal.cuh"
+#include "wq_ptx.cuh"
+
+namespace wq {
+
+__device__ unsigned int g_gemm_i8_timeout;
+
+namespace i8 {
+namespace {
+
+using namespace ptx;
+
+constexpr int kBK = 128;                         // bytes of K per stage: one swizzle row
+constexpr uint32_t kTile = 128 * kBK;            // a 128-row operand tile
+constexpr uint32_t kSmemMax = 227 * 1024;
+
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
+// 1024 bytes apart, sm_100 descriptor version 1.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | uint64_t(16u >> 4) << 16 | uint64_t(1024u >> 4) << 32 |
+         uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+// kind::i8: s32 accumulator, s8 A and B, both K-major.
+__host__ __device__ constexpr uint32_t i8_idesc(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+template <int CG>
+__device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs of the pair.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// A pair's copy into this CTA's shared memory that completes on the barrier at
+// cluster address `bar` (the leader's).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile uint32_t* abort) {
+  return mbar_try_wait(b, parity) || mbar_wait(b, parity, abort, &g_gemm_i8_timeout);
+}
+// 32 consecutive tensor-memory columns of this warp's 32 lanes, not waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Four neighbouring outputs of a row at element i; `vec`: rows start where a
+// store of four may.  Outputs from `n` on (of the four) are past the row.
+__device__ __forceinline__ void store_four(void* y, int64_t i, const float (&v)[4], int n, int type, bool vec) {
+  if (vec && n >= 4) {
+    if (type == kF32)
+      *reinterpret_cast<float4*>(static_cast<float*>(y) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + i) =
+          type == kBF16 ? make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]))
+                        : make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) store_one(y, i + j, v[j], type);
+  }
+}
+
+// ------------------------------------------------------------ split kernel
+
+struct alignas(64) SplitArgs {
+  CUtensorMap tx, t0, t1;
+  Linear L;
+  int mt;        // tokens of a tile: a multiple of 32, at most 256
+  int stages;
+  int vec;       // rows of y start where a store of four outputs may
+};
+
+constexpr int kSplitThreads = 128;
+constexpr int kSplitMax = 8;            // CTAs of a cluster along K
+constexpr int kMaxStages = 12;
+
+template <bool GATED>
+__global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __grid_constant__ SplitArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+  __shared__ uint32_t tmem_slot, abort_word;
+  volatile uint32_t* abort = &abort_word;
+  const Linear& L = p.L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.stages, mt = p.mt;
+  const uint32_t stage = kTile + uint32_t(mt) * kBK;
+  const int ks = gridDim.z, kr = blockIdx.z;
+  const int kb_all = int((L.K + kBK - 1) / kBK);
+  const int kb0 = int(int64_t(kb_all) * kr / ks), nkb = int(int64_t(kb_all) * (kr + 1) / ks) - kb0;
+  constexpr int kOut = GATED ? 64 : 128;          // outputs per token of a tile
+  const int64_t n0 = int64_t(blockIdx.x) * kOut, m0 = int64_t(blockIdx.y) * mt;
+  const uint32_t cols = mt <= 32 ? 32 : mt <= 64 ? 64 : mt <= 128 ? 128 : 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    *abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % S;
+        if (i >= S) ok = wait_for(&empty[s], ((i / S) - 1) & 1, abort);
+        if (!ok) break;
+        uint8_t* w = ring + s * stage;
+        const int k = (kb0 + i) * kBK;
+        mbar_expect_tx(&full[s], stage);
+        tma_load_2d(w, &p.t0, &full[s], k, int(n0));
+        if constexpr (GATED) tma_load_2d(w + kTile / 2, &p.t1, &full[s], k, int(n0));
+        tma_load_2d(w + kTile, &p.tx, &full[s], k, int(m0));
+        ++issued;
+      }
+      if (!ok)   // copies in flight land before shared memory goes away
+        for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+          mbar_drain(&full[i % S], (i / S) & 1, &g_gemm_i8_timeout);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = i8_idesc(128, mt);
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % S;
+        if (!wait_for(&full[s], (i / S) & 1, abort)) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(ring + s * stage), b = a + kTile;
+#pragma unroll
+        for (int kk = 0; kk < kBK; kk += 32)
+          umma_i8<1>(tmem, sw128_desc(a + kk), sw128_desc(b + kk), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        commit_one(&empty[s]);
+      }
+      commit_one(&done);   // always: the teardown waits on it before freeing tensor memory
+    }
+  }
+  __syncwarp();
+  bool ok = wait_for(&done, 0, abort);
+  ok = __all_sync(0xffffffffu, ok);   // tcgen05.ld needs the whole warp
+
+  // The int32 tile, [token][128 rows], into the idle ring; every MMA has read
+  // its operands and every copy has landed.
+  int* part = reinterpret_cast<int*>(ring);
+  if (ok) {
+    tc_fence_after();
+    for (int c = 0; c < mt; c += 32) {
+      uint32_t r[32];
+      tmem_ld32(tmem + (uint32_t(32 * warp) << 16) + uint32_t(c), r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) part[(c + j) * 128 + 32 * warp + lane] = int(r[j]);
+    }
+  }
+  __syncthreads();
+  if (ks > 1) cluster_sync();
+  // Rank kr sums tokens kr, kr + ks, ... over all ranks and stores them: a
+  // thread takes four neighbouring outputs of a token.
+  if (!*abort) {
+    constexpr int kGroups = kOut / 4, kTokens = kSplitThreads / kGroups;
+    const int j = threadIdx.x % kGroups;
+    const int64_t n = n0 + 4 * j;
+    const int left = int(min(int64_t(4), L.N - n));       // outputs of this thread inside the row
+    float s0[4], s1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s0[i] = i < left ? L.s0[n + i] : 0.0f;
+      s1[i] = GATED && i < left ? L.s1[n + i] : 0.0f;
+    }
+    const uint32_t pbase = smem_u32(part);
+    for (int m = kr + ks * (threadIdx.x / kGroups); m < mt && m0 + m < L.M; m += ks * kTokens) {
+      int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+      for (int r = 0; r < ks; ++r) {
+        const uint32_t at = pbase + uint32_t(m * 128 + 4 * j) * 4;
+        const uint32_t q = ks > 1 ? mapa(at, r) : at;
+        int4 v;
+        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(q)
+                     : "memory");
+        a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+        if constexpr (GATED) {
+          asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(q + 256)
+                       : "memory");
+          b[0] += v.x; b[1] += v.y; b[2] += v.z; b[3] += v.w;
+        }
+      }
+      const float sx = L.xs[m0 + m];
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = scaled(a[i], sx, s0[i]);
+        if constexpr (GATED) v[i] = apply_act(v[i], L.act) * scaled(b[i], sx, s1[i]);
+      }
+      if (left > 0) store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
+    }
+  }
+  if (ks > 1) {
+    __syncwarp();
+    cluster_sync();       // peers keep their tiles until read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (*abort) {
+      if (lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
+      __syncwarp();
+    }
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+  }
+}
+
+// ------------------------------------------------------------ pair kernel
+
+struct alignas(64) PairArgs {
+  CUtensorMap tx, t0, t1;
+  Linear L;
+  int bn;            // MMA columns of a tile: a multiple of 64, at most 256
+  int tiles_m, tiles_n;
+  int stages;
+  int vec;           // rows of y start on 16-byte boundaries
+};
+
+constexpr int kPairThreads = 192;       // producer, MMA, four epilogue warps
+constexpr int kPairStages = 6;
+constexpr int kGroupM = 16;             // token tiles that neighbouring tiles walk through first
+
+// Tile t -> (token tile, weight tile): groups of kGroupM token tiles, token
+// tiles fastest inside a group, so that the tiles in flight share operands.
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per = kGroupM * tiles_n, g = t / per, first = g * kGroupM;
+  const int rows = min(kGroupM, tiles_m - first), r = t - g * per;
+  tm = first + r % rows;
+  tn = r / rows;
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    gemm_i8_pair_kernel(const __grid_constant__ PairArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[kPairStages];      // leader's: both CTAs' copies landed
+  __shared__ uint64_t empty[kPairStages];     // MMAs done with the slot (commit to both)
+  __shared__ uint64_t acc_full[2];            // accumulator final (commit to both)
+  __shared__ uint64_t acc_empty[2];           // leader's: both CTAs' epilogue warps have read it
+  __shared__ uint64_t done;                   // all MMAs done (commit to both)
+  __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ float wscale_all[4][256];        // per epilogue warp: the tile's weight scales
+  volatile uint32_t* abort = &abort_word;
+  const Linear& L = p.L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int bn = p.bn, S = p.stages;
+  const uint32_t stage = kTile + uint32_t(bn / 2) * kBK;
+  const int nkb = int((L.K + kBK - 1) / kBK);
+  const int tiles = p.tiles_m * p.tiles_n, step = gridDim.x / 2;
+  const int out_n = GATED ? bn / 2 : bn;      // outputs per token of a tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 8);
+    }
+    mbar_init(&done, 1);
+    *abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();       // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      bool ok = true;
+      int i = 0;
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
+        int tm, tn;
+        tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+        const int mrow = tm * 256 + int(rank) * 128;
+        const int nrow = GATED ? tn * out_n : tn * bn + int(rank) * (bn / 2);
+        const CUtensorMap* tw = GATED && rank == 1 ? &p.t1 : &p.t0;
+        for (int kb = 0; kb < nkb; ++kb, ++i) {
+          const int s = i % S;
+          if (i >= S) ok = wait_for(&empty[s], ((i / S) - 1) & 1, abort);
+          if (!ok) break;
+          uint8_t* a = ring + s * stage;
+          const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * stage);
+          tma_load_pair(a, &p.tx, bar, kb * kBK, mrow);
+          tma_load_pair(a + kTile, tw, bar, kb * kBK, nrow);
+        }
+      }
+      // Given up: what is in flight lands before shared memory goes away.  The
+      // leader's barriers count both CTAs' bytes; the cluster barrier below
+      // keeps the peer until the leader is through.
+      if (!ok && rank == 0)
+        for (int j = i > S ? i - S : 0; j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1, &g_gemm_i8_timeout);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA (leader)
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = i8_idesc(256, bn);
+      bool ok = true;
+      int i = 0, n = 0;
+      for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
+        const int a = n & 1;
+        if (n >= 2) ok = wait_for(&acc_empty[a], ((n >> 1) - 1) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(a) * 256;
+        for (int kb = 0; kb < nkb; ++kb, ++i) {
+          const int s = i % S;
+          ok = wait_for(&full[s], (i / S) & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(ring + s * stage), sb = sa + kTile;
+#pragma unroll
+          for (int kk = 0; kk < kBK; kk += 32)
+            umma_i8<2>(d, sw128_desc(sa + kk), sw128_desc(sb + kk), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          commit_pair(&empty[s]);
+        }
+        if (ok) commit_pair(&acc_full[a]);
+      }
+      commit_pair(&done);   // always: both CTAs wait on it before they free tensor memory
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;                 // tensor-memory lanes 32 q ..: rows of this CTA's 128 tokens
+    float* wscale = wscale_all[q];
+    bool ok = true;
+    int n = 0;
+    for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
+      int tm, tn;
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int a = n & 1;
+      const int64_t m = int64_t(tm) * 256 + rank * 128 + 32 * q + lane;
+      const int64_t n0 = int64_t(tn) * out_n;
+      // the columns' scales (gated: the gate's, then the up projection's); each
+      // warp keeps its own, as no warp may wait for one that has given up
+      __syncwarp();
+      for (int c = lane; c < bn; c += 32) {
+        const int64_t nn = n0 + (GATED && c >= out_n ? c - out_n : c);
+        wscale[c] = nn < L.N ? (GATED && c >= out_n ? L.s1[nn] : L.s0[nn]) : 0.0f;
+      }
+      __syncwarp();
+      const float sx = m < L.M ? L.xs[m] : 0.0f;
+      ok = wait_for(&acc_full[a], (n >> 1) & 1, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t base = tmem + (uint32_t(32 * q) << 16) + uint32_t(a) * 256;
+      for (int c = 0; c < out_n; c += 32) {
+        uint32_t r[32], u[32];
+        tmem_ld32(base + uint32_t(c), r);
+        if constexpr (GATED) tmem_ld32(base + uint32_t(out_n + c), u);
+        tmem_wait_ld();
+        if (c + 32 >= out_n) {              // read to the end: the MMAs may have the accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(mapa(smem_u32(&acc_empty[a]), 0));
+        }
+        if (m < L.M) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[i] = scaled(int(r[j + i]), sx, wscale[c + j + i]);
+              if constexpr (GATED)
+                v[i] = apply_act(v[i], L.act) * scaled(int(u[j + i]), sx, wscale[out_n + c + j + i]);
+            }
+            const int64_t nn = n0 + c + j, at = m * L.ldy + nn;
+            if (p.vec && nn + 8 <= L.N) {
+              if (L.type == kF32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(L.y) + at);
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+              } else {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(L.y) + at) =
+                    L.type == kBF16 ? make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                 pack_bf16(v[6], v[7]))
+                                    : make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]),
+                                                 pack_f16(v[6], v[7]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (nn + i < L.N) store_one(L.y, at + i, v[i], L.type);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
+    __syncwarp();
+  }
+  cluster_sync();           // no arrival or copy of the pair is left in flight
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// ------------------------------------------------------------ host
+
+int sm_count(int dev) {
+  static std::atomic<int> cached[64];
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) n = 2;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Largest dynamic shared memory, once per kernel and device.
+template <typename F>
+cudaError_t allow_smem(F* fn, uint32_t bytes, std::atomic<bool>* set, int dev) {
+  if (set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, int(cudaSharedmemCarveoutMaxShared));
+  if (e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+bool make_map(CUtensorMap* map, const int8_t* base, int64_t K, int64_t rows, int64_t ld, int box_rows) {
+  return make_tensor_map_2d(map, TmaType::kU8, base, uint64_t(K), uint64_t(rows), uint64_t(ld), kBK,
+                            uint32_t(box_rows), 128);
+}
+
+cudaError_t current_device(int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return *dev >= 0 && *dev < 64 ? cudaSuccess : cudaErrorInvalidDevice;
+}
+
+template <bool GATED>
+cudaError_t split(const Linear& L, cudaStream_t st) {
+  int dev;
+  cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> set[64];
+  if ((e = allow_smem(gemm_i8_split_kernel<GATED>, kSmemMax - 4096, set, dev)) != cudaSuccess) return e;
+  const int nsm = sm_count(dev);
+  SplitArgs p;
+  p.L = L;
+  p.mt = int(L.M >= 256 ? 256 : (L.M + 31) / 32 * 32);
+  constexpr int kOut = GATED ? 64 : 128;
+  if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, kOut) ||
+      !make_map(&p.t1, GATED ? L.w1 : L.w0, L.K, L.N, L.ldw, kOut))
+    return cudaErrorInvalidValue;
+  const int eb = type_bytes(L.type);
+  p.vec = reinterpret_cast<uintptr_t>(L.y) % (4 * eb) == 0 && (L.ldy * eb) % (4 * eb) == 0;
+  const uint32_t stage = kTile + uint32_t(p.mt) * kBK;
+  const int per_sm = p.mt <= 128 ? 2 : 1;
+  const uint32_t budget = (kSmemMax / per_sm) - 4096;
+  p.stages = int((budget - 1024) / stage);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const int64_t tn = (L.N + kOut - 1) / kOut, tm = (L.M + p.mt - 1) / p.mt;
+  const int64_t kb = (L.K + kBK - 1) / kBK;
+  int ks = 1;
+  while (ks < kSplitMax && tn * tm * ks * 2 <= int64_t(nsm) * per_sm && kb >= 4 * ks) ks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tn), unsigned(tm), unsigned(ks));
+  cfg.blockDim = dim3(kSplitThreads, 1, 1);
+  cfg.dynamicSmemBytes = p.stages * stage + 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = unsigned(ks);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<GATED>, p);
+}
+
+template <bool GATED>
+cudaError_t pair(const Linear& L, cudaStream_t st) {
+  int dev;
+  cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> set[64];
+  if ((e = allow_smem(gemm_i8_pair_kernel<GATED>, kPairStages * 2 * kTile + 1024, set, dev)) != cudaSuccess) return e;
+  const int pairs = sm_count(dev) / 2;
+  PairArgs p;
+  p.L = L;
+  const int64_t tm = (L.M + 255) / 256;
+  double best = 1e300;
+  p.bn = 256;
+  for (int bn = 256; bn >= 64; bn -= 64) {
+    const int64_t tiles = tm * ((L.N + (GATED ? bn / 2 : bn) - 1) / (GATED ? bn / 2 : bn));
+    const double t = double((tiles + pairs - 1) / pairs) * (bn + 32);
+    if (t < best - 1e-9) {
+      best = t;
+      p.bn = bn;
+    }
+  }
+  const int out_n = GATED ? p.bn / 2 : p.bn;
+  const int64_t tn = (L.N + out_n - 1) / out_n;
+  if (tm * tn > 0x7fffffff) return cudaErrorInvalidValue;
+  p.tiles_m = int(tm);
+  p.tiles_n = int(tn);
+  if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, 128) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, p.bn / 2) ||
+      !make_map(&p.t1, GATED ? L.w1 : L.w0, L.K, L.N, L.ldw, p.bn / 2))
+    return cudaErrorInvalidValue;
+  const int eb = type_bytes(L.type);
+  p.vec = reinterpret_cast<uintptr_t>(L.y) % 16 == 0 && (L.ldy * eb) % 16 == 0;
+  const uint32_t stage = kTile + uint32_t(p.bn / 2) * kBK;
+  p.stages = kPairStages;
+  const int64_t ctas = 2 * (tm * tn < pairs ? tm * tn : pairs);
+  gemm_i8_pair_kernel<GATED><<<dim3(unsigned(ctas)), kPairThreads, p.stages * stage + 1024, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_split(const Linear& L, cudaStream_t st) {
+  return L.act == kNone ? split<false>(L, st) : split<true>(L, st);
+}
+cudaError_t launch_pair(const Linear& L, cudaStream_t st) {
+  return L.act == kNone ? pair<false>(L, st) : pair<true>(L, st);
+}
+
+cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
+  if (L.M <= 16) return launch_gemv(L, st);
+  if (L.M <= 256) return launch_split(L, st);
+  return launch_pair(L, st);
+}
+
+bool gemm_read_and_clear_timeout(cudaError_t* err) {
+  unsigned int v = 0;
+  const unsigned int zero = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_gemm_i8_timeout, sizeof(v));
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_gemm_i8_timeout, &zero, sizeof(zero));
+  *err = e;
+  return v != 0;
+}
+
+}  // namespace i8
+}  // namespace wq

@@ -65,9 +65,12 @@ __device__ __forceinline__ void store_one(void* y, int64_t i, float v, int type)
 cudaError_t launch_quantize(const void* x, int type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
                             int64_t ldc, float* scales, cudaStream_t st);
 cudaError_t launch_gemv(const Linear& L, cudaStream_t st);
+cudaError_t launch_split(const Linear& L, cudaStream_t st);
+cudaError_t launch_pair(const Linear& L, cudaStream_t st);
+bool gemm_read_and_clear_timeout(cudaError_t* err);
 
-// One call's kernel (arguments already checked by the C ABI).
-inline cudaError_t launch_linear(const Linear& L, cudaStream_t st) { return launch_gemv(L, st); }
+// The kernel of one call (arguments already checked by the C ABI).
+cudaError_t launch_linear(const Linear& L, cudaStream_t st);
 
 }  // namespace i8
 }  // namespace wq

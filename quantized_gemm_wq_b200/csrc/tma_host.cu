@@ -44,6 +44,7 @@ bool make_tensor_map_2d(void* map, TmaType type, const void* base, uint64_t inne
   }
   CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   if (type == TmaType::kBF16) dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (type == TmaType::kU8) dt = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return enc(static_cast<CUtensorMap*>(map), dt, 2, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE,
              swz,

@@ -347,10 +347,11 @@ wq_status wq_gated_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64
 }
 
 wq_status wq_last_device_error(void) {
-  cudaError_t e[6] = {cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess};
+  cudaError_t e[7] = {cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess, cudaSuccess};
   const bool hit = wq::gemm_tc_read_and_clear_timeout(&e[0]) | wq::gemv_m1_tma_read_and_clear_timeout(&e[1]) |
                    wq::gemv_tc_read_and_clear_timeout(&e[2]) | wq::gemv_mma_read_and_clear_timeout(&e[3]) |
-                   wq::gemv_grouped_read_and_clear_timeout(&e[4]) | wq::gemm_sw_read_and_clear_timeout(&e[5]);
+                   wq::gemv_grouped_read_and_clear_timeout(&e[4]) | wq::gemm_sw_read_and_clear_timeout(&e[5]) |
+                   wq::i8::gemm_read_and_clear_timeout(&e[6]);
   for (cudaError_t x : e)
     if (x != cudaSuccess) return WQ_ERR_CUDA;
   return hit ? WQ_ERR_DEVICE_TIMEOUT : WQ_OK;

@@ -118,7 +118,7 @@ bool gemv_tc_read_and_clear_timeout(cudaError_t* err);
 bool gemm_tc_read_and_clear_timeout(cudaError_t* err);
 
 // TMA tensor maps (a CUtensorMap is 128 bytes, 64-byte aligned).
-enum class TmaType { kU32, kBF16 };
+enum class TmaType { kU32, kBF16, kU8 };
 bool make_tensor_map_2d(void* map, TmaType type, const void* base, uint64_t inner, uint64_t outer,
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes);
 
