@@ -106,6 +106,19 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile uint32_t* abort) {
   return mbar_try_wait(b, parity) || mbar_wait(b, parity, abort, &g_gemm_i8_timeout);
 }
+// Position in a ring of `stages` slots: the slot and its round's parity, kept by
+// counting.  (The MMA thread has 512 cycles per stage: a division by the ring's
+// size, two descriptors built from scratch and the like took it past 800.)
+struct Slot {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
 // 32 consecutive tensor-memory columns of this warp's 32 lanes, not waited for.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -119,6 +132,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -155,7 +176,7 @@ struct alignas(64) SplitArgs {
   int vec;       // rows of y start where a store of four outputs may
 };
 
-constexpr int kSplitThreads = 128;
+constexpr int kSplitThreads = 256;
 constexpr int kSplitMax = 8;            // CTAs of a cluster along K
 constexpr int kMaxStages = 12;
 
@@ -165,6 +186,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
   __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ float xscale[256];
   volatile uint32_t* abort = &abort_word;
   const Linear& L = p.L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,16 +222,16 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
     if (lane == 0) {
       int issued = 0;
       bool ok = true;
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % S;
-        if (i >= S) ok = wait_for(&empty[s], ((i / S) - 1) & 1, abort);
+      Slot at;
+      for (int i = 0; i < nkb; ++i, at.next(S)) {
+        if (i >= S) ok = wait_for(&empty[at.s], at.parity ^ 1u, abort);
         if (!ok) break;
-        uint8_t* w = ring + s * stage;
+        uint8_t* w = ring + at.s * stage;
         const int k = (kb0 + i) * kBK;
-        mbar_expect_tx(&full[s], stage);
-        tma_load_2d(w, &p.t0, &full[s], k, int(n0));
-        if constexpr (GATED) tma_load_2d(w + kTile / 2, &p.t1, &full[s], k, int(n0));
-        tma_load_2d(w + kTile, &p.tx, &full[s], k, int(m0));
+        mbar_expect_tx(&full[at.s], stage);
+        tma_load_2d(w, &p.t0, &full[at.s], k, int(n0));
+        if constexpr (GATED) tma_load_2d(w + kTile / 2, &p.t1, &full[at.s], k, int(n0));
+        tma_load_2d(w + kTile, &p.tx, &full[at.s], k, int(m0));
         ++issued;
       }
       if (!ok)   // copies in flight land before shared memory goes away
@@ -219,20 +241,34 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = i8_idesc(128, mt);
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % S;
-        if (!wait_for(&full[s], (i / S) & 1, abort)) break;
+      const uint64_t ring_desc = sw128_desc(smem_u32(ring));
+      Slot at;
+      for (int i = 0; i < nkb; ++i, at.next(S)) {
+        if (!wait_for(&full[at.s], at.parity, abort)) break;
         tc_fence_after();
-        const uint32_t a = smem_u32(ring + s * stage), b = a + kTile;
+        const uint64_t a = ring_desc + uint32_t(at.s) * (stage >> 4), b = a + (kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kBK; kk += 32)
-          umma_i8<1>(tmem, sw128_desc(a + kk), sw128_desc(b + kk), idesc, (i > 0 || kk > 0) ? 1u : 0u);
-        commit_one(&empty[s]);
+        for (int kk = 0; kk < kBK / 32; ++kk)
+          umma_i8<1>(tmem, a + 2 * kk, b + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        commit_one(&empty[at.s]);
       }
       commit_one(&done);   // always: the teardown waits on it before freeing tensor memory
     }
   }
   __syncwarp();
+  // the scales of this thread's four outputs and of the tile's tokens, while
+  // the first operands are on their way
+  constexpr int kGroups = kOut / 4, kTokens = kSplitThreads / kGroups;
+  const int j = threadIdx.x % kGroups;
+  const int64_t n = n0 + 4 * j;
+  const int left = int(min(int64_t(4), L.N - n));       // outputs of this thread inside the row
+  float s0[4], s1[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s0[i] = i < left ? L.s0[n + i] : 0.0f;
+    s1[i] = GATED && i < left ? L.s1[n + i] : 0.0f;
+  }
+  if (threadIdx.x < mt) xscale[threadIdx.x] = m0 + threadIdx.x < L.M ? L.xs[m0 + threadIdx.x] : 0.0f;
   bool ok = wait_for(&done, 0, abort);
   ok = __all_sync(0xffffffffu, ok);   // tcgen05.ld needs the whole warp
 
@@ -241,57 +277,56 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
   int* part = reinterpret_cast<int*>(ring);
   if (ok) {
     tc_fence_after();
-    for (int c = 0; c < mt; c += 32) {
+    for (int c = 32 * (warp >> 2); c < mt; c += 64) {
       uint32_t r[32];
-      tmem_ld32(tmem + (uint32_t(32 * warp) << 16) + uint32_t(c), r);
+      tmem_ld32(tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(c), r);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; ++j) part[(c + j) * 128 + 32 * warp + lane] = int(r[j]);
+      for (int i = 0; i < 32; ++i) part[(c + i) * 128 + 32 * (warp & 3) + lane] = int(r[i]);
     }
   }
   __syncthreads();
   if (ks > 1) cluster_sync();
   // Rank kr sums tokens kr, kr + ks, ... over all ranks and stores them: a
-  // thread takes four neighbouring outputs of a token.
-  if (!*abort) {
-    constexpr int kGroups = kOut / 4, kTokens = kSplitThreads / kGroups;
-    const int j = threadIdx.x % kGroups;
-    const int64_t n = n0 + 4 * j;
-    const int left = int(min(int64_t(4), L.N - n));       // outputs of this thread inside the row
-    float s0[4], s1[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s0[i] = i < left ? L.s0[n + i] : 0.0f;
-      s1[i] = GATED && i < left ? L.s1[n + i] : 0.0f;
-    }
-    const uint32_t pbase = smem_u32(part);
-    for (int m = kr + ks * (threadIdx.x / kGroups); m < mt && m0 + m < L.M; m += ks * kTokens) {
-      int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  // thread takes four neighbouring outputs of a token, kBatch tokens at a time
+  // so that their loads are in flight together.
+  if (!*abort && left > 0) {
+    constexpr int kBatch = GATED ? 2 : 4;
+    const uint32_t pbase = smem_u32(part) + uint32_t(4 * j) * 4;
+    const int mend = int(min(int64_t(mt), L.M - m0));
+    for (int mb = kr + ks * (threadIdx.x / kGroups); mb < mend; mb += ks * kTokens * kBatch) {
+      int a[kBatch][4] = {}, b[kBatch][4] = {};
       for (int r = 0; r < ks; ++r) {
-        const uint32_t at = pbase + uint32_t(m * 128 + 4 * j) * 4;
-        const uint32_t q = ks > 1 ? mapa(at, r) : at;
-        int4 v;
-        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(q)
-                     : "memory");
-        a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
-        if constexpr (GATED) {
-          asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(q + 256)
-                       : "memory");
-          b[0] += v.x; b[1] += v.y; b[2] += v.z; b[3] += v.w;
+        int4 va[kBatch], vb[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int m = min(mb + i * ks * kTokens, mend - 1);
+          const uint32_t at = pbase + uint32_t(m) * 512;
+          const uint32_t q = ks > 1 ? mapa(at, r) : at;
+          va[i] = ld_cluster_int4(q);
+          if constexpr (GATED) vb[i] = ld_cluster_int4(q + 256);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          a[i][0] += va[i].x; a[i][1] += va[i].y; a[i][2] += va[i].z; a[i][3] += va[i].w;
+          if constexpr (GATED) {
+            b[i][0] += vb[i].x; b[i][1] += vb[i].y; b[i][2] += vb[i].z; b[i][3] += vb[i].w;
+          }
         }
       }
-      const float sx = L.xs[m0 + m];
-      float v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = scaled(a[i], sx, s0[i]);
-        if constexpr (GATED) v[i] = apply_act(v[i], L.act) * scaled(b[i], sx, s1[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int m = mb + i * ks * kTokens;
+        if (m >= mend) break;
+        const float sx = xscale[m];
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = scaled(a[i][e], sx, s0[e]);
+          if constexpr (GATED) v[e] = apply_act(v[e], L.act) * scaled(b[i][e], sx, s1[e]);
+        }
+        store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
       }
-      if (left > 0) store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
     }
   }
   if (ks > 1) {
@@ -321,7 +356,7 @@ struct alignas(64) PairArgs {
   int vec;           // rows of y start on 16-byte boundaries
 };
 
-constexpr int kPairThreads = 192;       // producer, MMA, four epilogue warps
+constexpr int kPairThreads = 320;       // producer, MMA, eight epilogue warps
 constexpr int kPairStages = 6;
 constexpr int kGroupM = 16;             // token tiles that neighbouring tiles walk through first
 
@@ -345,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ uint64_t acc_empty[2];           // leader's: both CTAs' epilogue warps have read it
   __shared__ uint64_t done;                   // all MMAs done (commit to both)
   __shared__ uint32_t tmem_slot, abort_word;
-  __shared__ float wscale_all[4][256];        // per epilogue warp: the tile's weight scales
+  __shared__ __align__(16) float wscale_all[8][256];   // per epilogue warp: the tile's weight scales
   volatile uint32_t* abort = &abort_word;
   const Linear& L = p.L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -363,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], 8);
+      mbar_init(&acc_empty[a], 16);
     }
     mbar_init(&done, 1);
     *abort = 0u;
@@ -385,19 +420,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int i = 0;
+      Slot at;
+      const uint32_t full0 = mapa(smem_u32(&full[0]), 0);      // the leader's barriers
       for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
         int tm, tn;
         tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
         const int mrow = tm * 256 + int(rank) * 128;
         const int nrow = GATED ? tn * out_n : tn * bn + int(rank) * (bn / 2);
         const CUtensorMap* tw = GATED && rank == 1 ? &p.t1 : &p.t0;
-        for (int kb = 0; kb < nkb; ++kb, ++i) {
-          const int s = i % S;
-          if (i >= S) ok = wait_for(&empty[s], ((i / S) - 1) & 1, abort);
+        for (int kb = 0; kb < nkb; ++kb, ++i, at.next(S)) {
+          if (i >= S) ok = wait_for(&empty[at.s], at.parity ^ 1u, abort);
           if (!ok) break;
-          uint8_t* a = ring + s * stage;
-          const uint32_t bar = mapa(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_expect_tx(&full[s], 2 * stage);
+          uint8_t* a = ring + at.s * stage;
+          const uint32_t bar = full0 + uint32_t(at.s) * 8;
+          if (rank == 0) mbar_expect_tx(&full[at.s], 2 * stage);
           tma_load_pair(a, &p.tx, bar, kb * kBK, mrow);
           tma_load_pair(a + kTile, tw, bar, kb * kBK, nrow);
         }
@@ -412,24 +448,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------------------ MMA (leader)
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = i8_idesc(256, bn);
+      const uint64_t ring_desc = sw128_desc(smem_u32(ring));
       bool ok = true;
-      int i = 0, n = 0;
+      int n = 0;
+      Slot at;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
         const int a = n & 1;
         if (n >= 2) ok = wait_for(&acc_empty[a], ((n >> 1) - 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(a) * 256;
-        for (int kb = 0; kb < nkb; ++kb, ++i) {
-          const int s = i % S;
-          ok = wait_for(&full[s], (i / S) & 1, abort);
+        for (int kb = 0; kb < nkb; ++kb, at.next(S)) {
+          ok = wait_for(&full[at.s], at.parity, abort);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(ring + s * stage), sb = sa + kTile;
+          const uint64_t sa = ring_desc + uint32_t(at.s) * (stage >> 4), sb = sa + (kTile >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBK; kk += 32)
-            umma_i8<2>(d, sw128_desc(sa + kk), sw128_desc(sb + kk), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-          commit_pair(&empty[s]);
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            umma_i8<2>(d, sa + 2 * kk, sb + 2 * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          commit_pair(&empty[at.s]);
         }
         if (ok) commit_pair(&acc_full[a]);
       }
@@ -437,8 +474,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;                 // tensor-memory lanes 32 q ..: rows of this CTA's 128 tokens
-    float* wscale = wscale_all[q];
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. (rows of this CTA's 128
+    // tokens), and of the 32-column blocks of outputs every other one.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    float* wscale = wscale_all[warp - 2];
     bool ok = true;
     int n = 0;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
@@ -461,25 +500,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + (uint32_t(32 * q) << 16) + uint32_t(a) * 256;
-      for (int c = 0; c < out_n; c += 32) {
+      for (int c = 32 * half;; c += 64) {
         uint32_t r[32], u[32];
-        tmem_ld32(base + uint32_t(c), r);
-        if constexpr (GATED) tmem_ld32(base + uint32_t(out_n + c), u);
-        tmem_wait_ld();
-        if (c + 32 >= out_n) {              // read to the end: the MMAs may have the accumulator
+        if (c < out_n) {
+          tmem_ld32(base + uint32_t(c), r);
+          if constexpr (GATED) tmem_ld32(base + uint32_t(out_n + c), u);
+          tmem_wait_ld();
+        }
+        if (c + 64 >= out_n) {              // this warp's columns are read: the MMAs may have the accumulator
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(mapa(smem_u32(&acc_empty[a]), 0));
         }
-        if (m < L.M) {
+        if (c < out_n && m < L.M) {
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v[i] = scaled(int(r[j + i]), sx, wscale[c + j + i]);
-              if constexpr (GATED)
-                v[i] = apply_act(v[i], L.act) * scaled(int(u[j + i]), sx, wscale[out_n + c + j + i]);
+            for (int i = 0; i < 8; i += 4) {
+              const float4 s0 = *reinterpret_cast<const float4*>(wscale + c + j + i);
+              v[i] = scaled(int(r[j + i]), sx, s0.x);
+              v[i + 1] = scaled(int(r[j + i + 1]), sx, s0.y);
+              v[i + 2] = scaled(int(r[j + i + 2]), sx, s0.z);
+              v[i + 3] = scaled(int(r[j + i + 3]), sx, s0.w);
+              if constexpr (GATED) {
+                const float4 s1 = *reinterpret_cast<const float4*>(wscale + out_n + c + j + i);
+                v[i] = apply_act(v[i], L.act) * scaled(int(u[j + i]), sx, s1.x);
+                v[i + 1] = apply_act(v[i + 1], L.act) * scaled(int(u[j + i + 1]), sx, s1.y);
+                v[i + 2] = apply_act(v[i + 2], L.act) * scaled(int(u[j + i + 2]), sx, s1.z);
+                v[i + 3] = apply_act(v[i + 3], L.act) * scaled(int(u[j + i + 3]), sx, s1.w);
+              }
             }
             const int64_t nn = n0 + c + j, at = m * L.ldy + nn;
             if (p.vec && nn + 8 <= L.N) {
@@ -501,6 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
         }
+        if (c + 64 >= out_n) break;
       }
     }
   }
