@@ -6,13 +6,13 @@
 // MMAs of K = 32 each.  Bytes past K and rows past the matrices read as zero.
 // int32 sums are exact, so a split of K needs no order.
 //
-// split kernel (a batch of up to 256 tokens): bound by the read of the
+// split kernel (a batch of up to 128 tokens): bound by the read of the
 //   weights.  128 weight rows (gated: 64 of the gate and the same 64 of the up
 //   projection) are the MMA's M side, the tokens, padded to a multiple of 32,
 //   its N side: every weight byte is read once.  K is split over a cluster
-//   when the tiles alone leave SMs idle; each rank parks its int32 tile in its
-//   own shared memory and sums a share of the tokens over all ranks through
-//   distributed shared memory.
+//   when the tiles alone leave SMs idle: rank r owns the tokens r, r + ks, ...;
+//   every rank writes its int32 sums of them into the owner's shared memory,
+//   and after one cluster barrier the owner adds what it holds.
 // pair kernel (larger batches): bound by the tensor cores.  Two SMs work on one
 //   tile of 256 tokens x BN weight rows (cta_group::2): each loads its 128
 //   tokens and half of the weight rows (gated: one SM the gate's, the other
@@ -103,6 +103,24 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Programmatic dependent launch: the next kernel of the stream may set itself
+// up from here on; this one touches no memory of its own before the kernels
+// ahead of it are complete.
+__device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile uint32_t* abort) {
   return mbar_try_wait(b, parity) || mbar_wait(b, parity, abort, &g_gemm_i8_timeout);
 }
@@ -132,14 +150,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -171,25 +181,26 @@ __device__ __forceinline__ void store_four(void* y, int64_t i, const float (&v)[
 struct alignas(64) SplitArgs {
   CUtensorMap tx, t0, t1;
   Linear L;
-  int mt;        // tokens of a tile: a multiple of 32, at most 256
+  int mt;        // tokens of a tile: a multiple of 32, at most kSplitTokens
   int stages;
   int vec;       // rows of y start where a store of four outputs may
 };
 
 constexpr int kSplitThreads = 256;
+constexpr int kSplitTokens = 128;
 constexpr int kSplitMax = 8;            // CTAs of a cluster along K
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 10;
 
 template <bool GATED>
-__global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __grid_constant__ SplitArgs p) {
+__global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const __grid_constant__ SplitArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
   __shared__ uint32_t tmem_slot, abort_word;
-  __shared__ float xscale[256];
+  __shared__ float xscale[kSplitTokens];
   volatile uint32_t* abort = &abort_word;
   const Linear& L = p.L;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int S = p.stages, mt = p.mt;
   const uint32_t stage = kTile + uint32_t(mt) * kBK;
   const int ks = gridDim.z, kr = blockIdx.z;
@@ -197,9 +208,13 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
   const int kb0 = int(int64_t(kb_all) * kr / ks), nkb = int(int64_t(kb_all) * (kr + 1) / ks) - kb0;
   constexpr int kOut = GATED ? 64 : 128;          // outputs per token of a tile
   const int64_t n0 = int64_t(blockIdx.x) * kOut, m0 = int64_t(blockIdx.y) * mt;
-  const uint32_t cols = mt <= 32 ? 32 : mt <= 64 ? 64 : mt <= 128 ? 128 : 256;
+  const uint32_t cols = mt <= 32 ? 32 : mt <= 64 ? 64 : 128;
 
+  pdl_start();
   if (threadIdx.x == 0) {
+    prefetch_map(&p.t0);
+    prefetch_map(&p.tx);
+    if constexpr (GATED) prefetch_map(&p.t1);
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -217,43 +232,47 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if (ks > 1) cluster_arrive();        // waited for before the first write to a peer: it runs by then
+  pdl_wait();
 
+  // Warps 0 and 1 stay whole, so that what they compute for the one issuing
+  // lane lives in uniform registers, where the TMA and MMA instructions read it.
   if (warp == 0) {
-    if (lane == 0) {
-      int issued = 0;
-      bool ok = true;
-      Slot at;
-      for (int i = 0; i < nkb; ++i, at.next(S)) {
-        if (i >= S) ok = wait_for(&empty[at.s], at.parity ^ 1u, abort);
-        if (!ok) break;
-        uint8_t* w = ring + at.s * stage;
-        const int k = (kb0 + i) * kBK;
+    int issued = 0;
+    bool ok = true;
+    Slot at;
+    for (int i = 0; i < nkb; ++i, at.next(S)) {
+      if (i >= S) ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort));
+      if (!ok) break;
+      uint8_t* w = ring + at.s * stage;
+      const int k = (kb0 + i) * kBK;
+      if (elect_one()) {
         mbar_expect_tx(&full[at.s], stage);
         tma_load_2d(w, &p.t0, &full[at.s], k, int(n0));
         if constexpr (GATED) tma_load_2d(w + kTile / 2, &p.t1, &full[at.s], k, int(n0));
         tma_load_2d(w + kTile, &p.tx, &full[at.s], k, int(m0));
-        ++issued;
       }
-      if (!ok)   // copies in flight land before shared memory goes away
-        for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-          mbar_drain(&full[i % S], (i / S) & 1, &g_gemm_i8_timeout);
+      ++issued;
     }
+    if (!ok && lane == 0)   // copies in flight land before shared memory goes away
+      for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+        mbar_drain(&full[i % S], (i / S) & 1, &g_gemm_i8_timeout);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = i8_idesc(128, mt);
-      const uint64_t ring_desc = sw128_desc(smem_u32(ring));
-      Slot at;
-      for (int i = 0; i < nkb; ++i, at.next(S)) {
-        if (!wait_for(&full[at.s], at.parity, abort)) break;
-        tc_fence_after();
-        const uint64_t a = ring_desc + uint32_t(at.s) * (stage >> 4), b = a + (kTile >> 4);
+    const uint32_t idesc = i8_idesc(128, mt);
+    const uint64_t ring_desc = sw128_desc(smem_u32(ring));
+    Slot at;
+    for (int i = 0; i < nkb; ++i, at.next(S)) {
+      if (!__all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort))) break;
+      tc_fence_after();
+      const uint64_t a = ring_desc + uint32_t(at.s) * (stage >> 4), b = a + (kTile >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk)
           umma_i8<1>(tmem, a + 2 * kk, b + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
         commit_one(&empty[at.s]);
       }
-      commit_one(&done);   // always: the teardown waits on it before freeing tensor memory
     }
+    if (elect_one()) commit_one(&done);   // always: the teardown waits on it before freeing tensor memory
   }
   __syncwarp();
   // the scales of this thread's four outputs and of the tile's tokens, while
@@ -272,66 +291,61 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_i8_split_kernel(const __gr
   bool ok = wait_for(&done, 0, abort);
   ok = __all_sync(0xffffffffu, ok);   // tcgen05.ld needs the whole warp
 
-  // The int32 tile, [token][128 rows], into the idle ring; every MMA has read
-  // its operands and every copy has landed.
-  int* part = reinterpret_cast<int*>(ring);
+  // The int32 sums as [rank][own token][128 rows]: with one rank in the idle
+  // ring (every MMA has read its operands and every copy has landed), with
+  // more behind the ring of each token's owner.
+  int* part = reinterpret_cast<int*>(ks > 1 ? ring + S * stage : ring);
+  const int own = mt / ks;             // tokens a rank owns
+  if (ks > 1) cluster_wait();
   if (ok) {
     tc_fence_after();
+    const uint32_t row = smem_u32(part) + uint32_t(32 * (warp & 3) + lane) * 4;
     for (int c = 32 * (warp >> 2); c < mt; c += 64) {
       uint32_t r[32];
       tmem_ld32(tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(c), r);
       tmem_wait_ld();
+      if (ks == 1) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) part[(c + i) * 128 + 32 * (warp & 3) + lane] = int(r[i]);
+        for (int i = 0; i < 32; ++i) part[(c + i) * 128 + 32 * (warp & 3) + lane] = int(r[i]);
+      } else {
+        // ks divides 32: token c + i belongs to rank i % ks
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          st_cluster(mapa(row + uint32_t(kr * own + (c + i) / ks) * 512, uint32_t(i & (ks - 1))), r[i]);
+      }
     }
   }
   __syncthreads();
-  if (ks > 1) cluster_sync();
-  // Rank kr sums tokens kr, kr + ks, ... over all ranks and stores them: a
-  // thread takes four neighbouring outputs of a token, kBatch tokens at a time
-  // so that their loads are in flight together.
+  if (ks > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  // A thread takes four neighbouring outputs of a token; token t of this rank
+  // is row kr + ks t of the tile.
   if (!*abort && left > 0) {
-    constexpr int kBatch = GATED ? 2 : 4;
-    const uint32_t pbase = smem_u32(part) + uint32_t(4 * j) * 4;
     const int mend = int(min(int64_t(mt), L.M - m0));
-    for (int mb = kr + ks * (threadIdx.x / kGroups); mb < mend; mb += ks * kTokens * kBatch) {
-      int a[kBatch][4] = {}, b[kBatch][4] = {};
-      for (int r = 0; r < ks; ++r) {
-        int4 va[kBatch], vb[kBatch];
+    for (int t = threadIdx.x / kGroups; kr + ks * t < mend; t += kTokens) {
+      int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int m = min(mb + i * ks * kTokens, mend - 1);
-          const uint32_t at = pbase + uint32_t(m) * 512;
-          const uint32_t q = ks > 1 ? mapa(at, r) : at;
-          va[i] = ld_cluster_int4(q);
-          if constexpr (GATED) vb[i] = ld_cluster_int4(q + 256);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          a[i][0] += va[i].x; a[i][1] += va[i].y; a[i][2] += va[i].z; a[i][3] += va[i].w;
+      for (int r = 0; r < kSplitMax; ++r)
+        if (r < ks) {
+          const int4 v = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + 4 * j);
+          a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
           if constexpr (GATED) {
-            b[i][0] += vb[i].x; b[i][1] += vb[i].y; b[i][2] += vb[i].z; b[i][3] += vb[i].w;
+            const int4 u = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + 64 + 4 * j);
+            b[0] += u.x; b[1] += u.y; b[2] += u.z; b[3] += u.w;
           }
         }
-      }
+      const int m = kr + ks * t;
+      const float sx = xscale[m];
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int m = mb + i * ks * kTokens;
-        if (m >= mend) break;
-        const float sx = xscale[m];
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = scaled(a[i][e], sx, s0[e]);
-          if constexpr (GATED) v[e] = apply_act(v[e], L.act) * scaled(b[i][e], sx, s1[e]);
-        }
-        store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
+      for (int e = 0; e < 4; ++e) {
+        v[e] = scaled(a[e], sx, s0[e]);
+        if constexpr (GATED) v[e] = apply_act(v[e], L.act) * scaled(b[e], sx, s1[e]);
       }
+      store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
     }
-  }
-  if (ks > 1) {
-    __syncwarp();
-    cluster_sync();       // peers keep their tiles until read
   }
   tc_fence_before();
   __syncthreads();
@@ -360,6 +374,37 @@ constexpr int kPairThreads = 320;       // producer, MMA, eight epilogue warps
 constexpr int kPairStages = 6;
 constexpr int kGroupM = 16;             // token tiles that neighbouring tiles walk through first
 
+// A warp's 32 rows of 64 output bytes, from its staging buffer to columns n ..
+// of rows m .. of y: rows of 64 bytes by 16-byte stores where y's rows allow
+// them, else by elements, neighbouring lanes to neighbouring addresses.
+// (Stored straight from the lanes that hold a row each, a store touches 32
+// rows: 1.1 us per 32 columns, and 32-fold traffic where rows are unaligned.)
+constexpr int kOutRow = 80;
+__device__ __forceinline__ void flush_rows(const uint8_t* out, const Linear& L, int64_t m, int64_t n, int lane, int vec) {
+  __syncwarp();
+  const int eb = L.type == kF32 ? 4 : 2, cols = 64 / eb;
+  uint8_t* y = static_cast<uint8_t*>(L.y);
+  if (vec && n + cols <= L.N) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * i + lane / 4, at = (lane & 3) * 16;
+      if (m + row < L.M)
+        *reinterpret_cast<uint4*>(y + ((m + row) * L.ldy + n) * eb + at) =
+            *reinterpret_cast<const uint4*>(out + row * kOutRow + at);
+    }
+  } else {
+    const int col = lane & (cols - 1), per = 32 / cols;
+    if (n + col < L.N)
+      for (int row = lane / cols; row < 32 && m + row < L.M; row += per) {
+        const uint8_t* src = out + row * kOutRow + col * eb;
+        uint8_t* dst = y + ((m + row) * L.ldy + n + col) * eb;
+        if (eb == 4) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+        else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+      }
+  }
+  __syncwarp();
+}
+
 // Tile t -> (token tile, weight tile): groups of kGroupM token tiles, token
 // tiles fastest inside a group, so that the tiles in flight share operands.
 __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
@@ -380,10 +425,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ uint64_t acc_empty[2];           // leader's: both CTAs' epilogue warps have read it
   __shared__ uint64_t done;                   // all MMAs done (commit to both)
   __shared__ uint32_t tmem_slot, abort_word;
-  __shared__ __align__(16) float wscale_all[8][256];   // per epilogue warp: the tile's weight scales
+  // per epilogue warp: the tile's weight scales; 32 rows of 64 output bytes, 16 bytes apart
+  __shared__ __align__(16) float wscale_all[8][256];
+  __shared__ __align__(16) uint8_t out_all[8][32 * kOutRow];
   volatile uint32_t* abort = &abort_word;
   const Linear& L = p.L;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int bn = p.bn, S = p.stages;
   const uint32_t stage = kTile + uint32_t(bn / 2) * kBK;
@@ -391,7 +438,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int tiles = p.tiles_m * p.tiles_n, step = gridDim.x / 2;
   const int out_n = GATED ? bn / 2 : bn;      // outputs per token of a tile
 
+  pdl_start();
   if (threadIdx.x == 0) {
+    prefetch_map(&p.tx);
+    prefetch_map(GATED && rank == 1 ? &p.t1 : &p.t0);
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -415,38 +465,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
+  pdl_wait();
+
+  // Warps 0 and 1 stay whole, so that what they compute for the one issuing
+  // lane lives in uniform registers, where the TMA and MMA instructions read it
+  // (with a lone lane the MMA warp needed over 600 cycles a stage of 512).
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      bool ok = true;
-      int i = 0;
-      Slot at;
-      const uint32_t full0 = mapa(smem_u32(&full[0]), 0);      // the leader's barriers
-      for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
-        int tm, tn;
-        tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
-        const int mrow = tm * 256 + int(rank) * 128;
-        const int nrow = GATED ? tn * out_n : tn * bn + int(rank) * (bn / 2);
-        const CUtensorMap* tw = GATED && rank == 1 ? &p.t1 : &p.t0;
-        for (int kb = 0; kb < nkb; ++kb, ++i, at.next(S)) {
-          if (i >= S) ok = wait_for(&empty[at.s], at.parity ^ 1u, abort);
-          if (!ok) break;
-          uint8_t* a = ring + at.s * stage;
-          const uint32_t bar = full0 + uint32_t(at.s) * 8;
+    bool ok = true;
+    int i = 0;
+    Slot at;
+    const uint32_t full0 = mapa(smem_u32(&full[0]), 0);      // the leader's barriers
+    const CUtensorMap* tw = GATED && rank == 1 ? &p.t1 : &p.t0;
+    for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
+      int tm, tn;
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int mrow = tm * 256 + int(rank) * 128;
+      const int nrow = GATED ? tn * out_n : tn * bn + int(rank) * (bn / 2);
+      for (int kb = 0; kb < nkb; ++kb, ++i, at.next(S)) {
+        if (i >= S) ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort));
+        if (!ok) break;
+        uint8_t* a = ring + at.s * stage;
+        const uint32_t bar = full0 + uint32_t(at.s) * 8;
+        if (elect_one()) {
           if (rank == 0) mbar_expect_tx(&full[at.s], 2 * stage);
           tma_load_pair(a, &p.tx, bar, kb * kBK, mrow);
           tma_load_pair(a + kTile, tw, bar, kb * kBK, nrow);
         }
       }
-      // Given up: what is in flight lands before shared memory goes away.  The
-      // leader's barriers count both CTAs' bytes; the cluster barrier below
-      // keeps the peer until the leader is through.
-      if (!ok && rank == 0)
-        for (int j = i > S ? i - S : 0; j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1, &g_gemm_i8_timeout);
     }
+    // Given up: what is in flight lands before shared memory goes away.  The
+    // leader's barriers count both CTAs' bytes; the cluster barrier below
+    // keeps the peer until the leader is through.
+    if (!ok && rank == 0 && lane == 0)
+      for (int j = i > S ? i - S : 0; j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1, &g_gemm_i8_timeout);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA (leader)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = i8_idesc(256, bn);
       const uint64_t ring_desc = sw128_desc(smem_u32(ring));
       bool ok = true;
@@ -454,23 +509,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       Slot at;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
         const int a = n & 1;
-        if (n >= 2) ok = wait_for(&acc_empty[a], ((n >> 1) - 1) & 1, abort);
+        if (n >= 2) ok = __all_sync(0xffffffffu, wait_for(&acc_empty[a], ((n >> 1) - 1) & 1, abort));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(a) * 256;
         for (int kb = 0; kb < nkb; ++kb, at.next(S)) {
-          ok = wait_for(&full[at.s], at.parity, abort);
+          ok = __all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort));
           if (!ok) break;
           tc_fence_after();
           const uint64_t sa = ring_desc + uint32_t(at.s) * (stage >> 4), sb = sa + (kTile >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            umma_i8<2>(d, sa + 2 * kk, sb + 2 * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-          commit_pair(&empty[at.s]);
+            for (int kk = 0; kk < kBK / 32; ++kk)
+              umma_i8<2>(d, sa + 2 * kk, sb + 2 * kk, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            commit_pair(&empty[at.s]);
+          }
         }
-        if (ok) commit_pair(&acc_full[a]);
+        if (ok && elect_one()) commit_pair(&acc_full[a]);
       }
-      commit_pair(&done);   // always: both CTAs wait on it before they free tensor memory
+      if (elect_one()) commit_pair(&done);   // always: both CTAs wait on it before they free tensor memory
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -478,6 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // tokens), and of the 32-column blocks of outputs every other one.
     const int q = warp & 3, half = (warp - 2) >> 2;
     float* wscale = wscale_all[warp - 2];
+    uint8_t* out = out_all[warp - 2];
     bool ok = true;
     int n = 0;
     for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
@@ -512,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_cluster(mapa(smem_u32(&acc_empty[a]), 0));
         }
-        if (c < out_n && m < L.M) {
+        if (c < out_n) {
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
             float v[8];
@@ -531,25 +589,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 v[i + 3] = apply_act(v[i + 3], L.act) * scaled(int(u[j + i + 3]), sx, s1.w);
               }
             }
-            const int64_t nn = n0 + c + j, at = m * L.ldy + nn;
-            if (p.vec && nn + 8 <= L.N) {
-              if (L.type == kF32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(L.y) + at);
-                o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                o[1] = make_float4(v[4], v[5], v[6], v[7]);
-              } else {
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(L.y) + at) =
-                    L.type == kBF16 ? make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                 pack_bf16(v[6], v[7]))
-                                    : make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]),
-                                                 pack_f16(v[6], v[7]));
-              }
+            if (L.type == kF32) {
+              uint4* o = reinterpret_cast<uint4*>(out + lane * kOutRow + (j & 8) * 4);
+              o[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+              o[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+              if (j & 8) flush_rows(out, L, m - lane, n0 + c + j - 8, lane, p.vec);
             } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (nn + i < L.N) store_one(L.y, at + i, v[i], L.type);
+              *reinterpret_cast<uint4*>(out + lane * kOutRow + j * 2) =
+                  L.type == kBF16 ? make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                               pack_bf16(v[6], v[7]))
+                                  : make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]),
+                                               pack_f16(v[6], v[7]));
             }
           }
+          if (L.type != kF32) flush_rows(out, L, m - lane, n0 + c, lane, p.vec);
         }
         if (c + 64 >= out_n) break;
       }
@@ -615,7 +668,7 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   const int nsm = sm_count(dev);
   SplitArgs p;
   p.L = L;
-  p.mt = int(L.M >= 256 ? 256 : (L.M + 31) / 32 * 32);
+  p.mt = int(L.M >= kSplitTokens ? kSplitTokens : (L.M + 31) / 32 * 32);
   constexpr int kOut = GATED ? 64 : 128;
   if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, kOut) ||
       !make_map(&p.t1, GATED ? L.w1 : L.w0, L.K, L.N, L.ldw, kOut))
@@ -623,26 +676,30 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   const int eb = type_bytes(L.type);
   p.vec = reinterpret_cast<uintptr_t>(L.y) % (4 * eb) == 0 && (L.ldy * eb) % (4 * eb) == 0;
   const uint32_t stage = kTile + uint32_t(p.mt) * kBK;
-  const int per_sm = p.mt <= 128 ? 2 : 1;
-  const uint32_t budget = (kSmemMax / per_sm) - 4096;
-  p.stages = int((budget - 1024) / stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int64_t tn = (L.N + kOut - 1) / kOut, tm = (L.M + p.mt - 1) / p.mt;
+  if (tm > 65535) return cudaErrorInvalidValue;
   const int64_t kb = (L.K + kBK - 1) / kBK;
   int ks = 1;
-  while (ks < kSplitMax && tn * tm * ks * 2 <= int64_t(nsm) * per_sm && kb >= 4 * ks) ks *= 2;
+  while (ks < kSplitMax && tn * tm * ks * 8 <= int64_t(nsm) * 5 && kb >= 4 * ks) ks *= 2;
+  const uint32_t parked = ks > 1 ? uint32_t(p.mt) * 512 : 0;
+  const uint32_t budget = (tn * tm * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
+  p.stages = int((budget - 1024 - parked) / stage);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  if (p.stages < 2 || p.stages * stage < uint32_t(p.mt) * 512) p.stages = int((kSmemMax - 4096 - 1024 - parked) / stage);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tn), unsigned(tm), unsigned(ks));
   cfg.blockDim = dim3(kSplitThreads, 1, 1);
-  cfg.dynamicSmemBytes = p.stages * stage + 1024;
+  cfg.dynamicSmemBytes = p.stages * stage + parked + 1024;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = unsigned(ks);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = unsigned(ks);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ks > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<GATED>, p);
 }
 
@@ -680,8 +737,17 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
   const uint32_t stage = kTile + uint32_t(p.bn / 2) * kBK;
   p.stages = kPairStages;
   const int64_t ctas = 2 * (tm * tn < pairs ? tm * tn : pairs);
-  gemm_i8_pair_kernel<GATED><<<dim3(unsigned(ctas)), kPairThreads, p.stages * stage + 1024, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = p.stages * stage + 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel<GATED>, p);
 }
 
 }  // namespace
@@ -695,7 +761,7 @@ cudaError_t launch_pair(const Linear& L, cudaStream_t st) {
 
 cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
   if (L.M <= 16) return launch_gemv(L, st);
-  if (L.M <= 256) return launch_split(L, st);
+  if (L.M <= kSplitTokens) return launch_split(L, st);
   return launch_pair(L, st);
 }
 

@@ -38,14 +38,16 @@ struct Linear {
 };
 
 // act(g).  Forms without cancellation: for g << 0 the result keeps its
-// relative accuracy (1 + erf would lose it), for g << 0 in silu the division
-// by an overflowed exponential gives -0, the limit.
+// relative accuracy (1 + erf or 1 + tanh would lose it).  Where exp(-g) passes
+// 2^126 the quotient is 0, for a true |act| below |g| 2^-126.  The hardware's
+// exponential and division (2 + 1.2 |g| and 2 steps) stand for expf and the
+// IEEE division, whose instructions held up a gated tile's epilogue.
 __device__ __forceinline__ float apply_act(float g, int act) {
-  if (act == kSilu) return g / (1.0f + expf(-g));
+  if (act == kSilu) return __fdividef(g, 1.0f + __expf(-g));
   if (act == kGelu) return 0.5f * g * erfcf(g * -0.70710678118654752f);
   // g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)) = 0.5 g (1 + tanh(...))
   const float t = 1.5957691216057308f * (g + 0.044715f * g * g * g);
-  return g / (1.0f + expf(-t));
+  return __fdividef(g, 1.0f + __expf(-t));
 }
 
 // acc s_x s_w, scaled in that order: s_x s_w alone could leave fp32's range

@@ -45,13 +45,14 @@ def gated_ref(accg, accu, xs, gs, us, act):
     g and u carry three roundings each (3 U relative).  d(act)/act <= c |dg/g|
     with c = 1 + |g| (silu), 2 + g^2 (gelu: |z erfc'(z) / erfc(z)| <= 1 + 2 z^2
     at z = |g| / sqrt 2, one more for the factor g) and 1 + 3 |t| (gelu_tanh:
-    |dt/t| <= 3 |dg/g|).  The activation itself, in units of U: expf 2 steps
-    = 4, the sum 1, the division 1, t's own evaluation 8 |t|; erfcf 4 steps =
-    8, its argument 2 (1 + g^2), two products 2.  The product with u: 3 + 1.
-    Far below zero the activation leaves fp32's normal range: where exp(-g) (or
-    exp(-t)) passes 2^128 the quotient is 0 for a true |act| < |g| 2^-128, and
-    above that a result under 2^-126 is off by up to 2^-149: together at most
-    (|g| + 1) 2^-127 |u|, and 2^-126 for the product's own underflow."""
+    |dt/t| <= 3 |dg/g|).  The activation itself, in units of U: the hardware's
+    exponential of v, 2 + 1.173 |v| steps (the CUDA guide's bound) = 4 + 2.4 |v|,
+    the sum 1, its division 2 steps = 4, t's own evaluation 8 |t|; erfcf 4 steps
+    = 8, its argument 2 (1 + g^2), two products 2.  The product with u: 3 + 1.
+    Far below zero the activation leaves fp32's normal range: where 1 + exp(-g)
+    (or exp(-t)) passes 2^126 the hardware's quotient is 0, for a true |act| <
+    |g| 2^-126, and one under 2^-126 may be flushed: together at most
+    (|g| + 1) 2^-126 |u|, and 2^-126 for the product's own underflow."""
     import math
     import torch as t
     g = accg * xs[:, None].astype(np.float64) * gs[None, :].astype(np.float64)
@@ -59,16 +60,16 @@ def gated_ref(accg, accu, xs, gs, us, act):
     gt = t.from_numpy(g)
     if act == "silu":
         a = (gt * t.sigmoid(gt)).numpy()
-        units = 3 * (1 + np.abs(g)) + 6
+        units = 3 * (1 + np.abs(g)) + 4 + 2.4 * np.abs(g) + 1 + 4
     elif act == "gelu":
         a = (0.5 * gt * t.special.erfc(-gt / math.sqrt(2.0))).numpy()
         units = 3 * (2 + g * g) + 8 + 2 * (1 + g * g) + 2
     else:
         tt = 2.0 * math.sqrt(2.0 / math.pi) * (g + 0.044715 * g ** 3)
         a = g / (1.0 + np.exp(-np.clip(tt, -700, 700)))
-        units = 3 * (1 + 3 * np.abs(tt)) + 6 + 8 * np.abs(tt)
+        units = 3 * (1 + 3 * np.abs(tt)) + 4 + 2.4 * np.abs(tt) + 1 + 4 + 8 * np.abs(tt)
     h = a * u
-    return h, np.abs(h) * (units + 4) * U * 1.01 + 2.0 ** -126 + (np.abs(g) + 1) * 2.0 ** -127 * np.abs(u)
+    return h, np.abs(h) * (units + 4) * U * 1.01 + 2.0 ** -126 + (np.abs(g) + 1) * 2.0 ** -126 * np.abs(u)
 
 
 def assert_rounds_to(y: torch.Tensor, ref: np.ndarray, err: np.ndarray, what=""):
