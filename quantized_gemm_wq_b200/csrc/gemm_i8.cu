@@ -116,11 +116,6 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-// Programmatic dependent launch: the next kernel of the stream may set itself
-// up from here on; this one touches no memory of its own before the kernels
-// ahead of it are complete.
-__device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile uint32_t* abort) {
   return mbar_try_wait(b, parity) || mbar_wait(b, parity, abort, &g_gemm_i8_timeout);
 }
@@ -364,7 +359,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
 struct alignas(64) PairArgs {
   CUtensorMap tx, t0, t1;
   Linear L;
-  int bn;            // MMA columns of a tile: a multiple of 64, at most 256
+  int bn;            // MMA columns of a tile: a multiple of 32 (gated: 64), at most 256
   int tiles_m, tiles_n;
   int stages;
   int vec;           // rows of y start on 16-byte boundaries
@@ -680,7 +675,7 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   if (tm > 65535) return cudaErrorInvalidValue;
   const int64_t kb = (L.K + kBK - 1) / kBK;
   int ks = 1;
-  while (ks < kSplitMax && tn * tm * ks * 8 <= int64_t(nsm) * 5 && kb >= 4 * ks) ks *= 2;
+  while (ks < kSplitMax && tn * tm * ks * 2 <= nsm && kb >= 4 * ks) ks *= 2;
   const uint32_t parked = ks > 1 ? uint32_t(p.mt) * 512 : 0;
   const uint32_t budget = (tn * tm * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
   p.stages = int((budget - 1024 - parked) / stage);
@@ -716,7 +711,7 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
   const int64_t tm = (L.M + 255) / 256;
   double best = 1e300;
   p.bn = 256;
-  for (int bn = 256; bn >= 64; bn -= 64) {
+  for (int bn = 256; bn >= 64; bn -= GATED ? 64 : 32) {
     const int64_t tiles = tm * ((L.N + (GATED ? bn / 2 : bn) - 1) / (GATED ? bn / 2 : bn));
     const double t = double((tiles + pairs - 1) / pairs) * (bn + 32);
     if (t < best - 1e-9) {
@@ -760,7 +755,7 @@ cudaError_t launch_pair(const Linear& L, cudaStream_t st) {
 }
 
 cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
-  if (L.M <= 16) return launch_gemv(L, st);
+  if (L.M <= 8) return launch_gemv(L, st);
   if (L.M <= kSplitTokens) return launch_split(L, st);
   return launch_pair(L, st);
 }

@@ -10,8 +10,8 @@
 // go straight from memory to registers; nothing is staged.
 //
 // One CTA computes 16 output rows (of both projections in a gated call) for
-// its block of tokens; its warps take the 64-byte chunks of K in turn and
-// their int32 sums meet in shared memory.
+// all tokens; its warps take the 64-byte chunks of K in turn, several chunks'
+// loads in flight each, and their int32 sums meet in shared memory.
 #include "i8.cuh"
 #include "wq_internal.cuh"
 
@@ -20,6 +20,7 @@ namespace i8 {
 namespace {
 
 constexpr int kMaxWarps = 16;
+constexpr int kTokens = 8;
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
@@ -46,15 +47,15 @@ __device__ __forceinline__ uint4 ld_part(const int8_t* p, int valid) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// NT: blocks of 8 tokens; RT: tiles of 16 rows (gated: the gate's and the up
-// projection's); U: chunks in flight per warp.
-template <int NT, bool GATED, int U>
+// U: chunks in flight per warp.
+template <bool GATED, int U>
 __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L) {
-  constexpr int RT = GATED ? 2 : 1;
-  extern __shared__ int red[];   // [warp][RT][NT * 8 tokens][16 rows]
+  constexpr int RT = GATED ? 2 : 1;    // tiles of 16 rows: the gate's and the up projection's
+  __shared__ int red[kMaxWarps][RT][kTokens][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * (8 * NT);
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  pdl_start();
 
   const int8_t* wp[RT][2];
 #pragma unroll
@@ -63,98 +64,93 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L)
     wp[0][h] = L.w0 + n * L.ldw + 16 * t;
     if constexpr (GATED) wp[1][h] = L.w1 + n * L.ldw + 16 * t;
   }
-  const int8_t* xp[NT];
-  bool xlive[NT];
+  const bool xlive = g < L.M;
+  const int8_t* xp = L.x + (xlive ? g : 0) * L.ldx + 16 * t;
+  int acc[RT][4] = {};
+  auto feed = [&](const uint4 (&a)[RT][2], const uint4& x) {
 #pragma unroll
-  for (int b = 0; b < NT; ++b) {
-    const int64_t m = m0 + 8 * b + g;
-    xlive[b] = m < L.M;
-    xp[b] = L.x + (xlive[b] ? m : 0) * L.ldx + 16 * t;
-  }
-  int acc[RT][NT][4] = {};
-  auto feed = [&](const uint4 (&a)[RT][2], const uint4 (&x)[NT]) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        mma_s8(acc[r][b], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y, x[b].x, x[b].y);
-        mma_s8(acc[r][b], a[r][0].z, a[r][1].z, a[r][0].w, a[r][1].w, x[b].z, x[b].w);
-      }
+    for (int r = 0; r < RT; ++r) {
+      mma_s8(acc[r], a[r][0].x, a[r][1].x, a[r][0].y, a[r][1].y, x.x, x.y);
+      mma_s8(acc[r], a[r][0].z, a[r][1].z, a[r][0].w, a[r][1].w, x.z, x.w);
+    }
   };
+  pdl_wait();
 
-  const int64_t chunks = L.K / 64;
-  int64_t c = warp;
-  for (; c + int64_t(U - 1) * warps < chunks; c += int64_t(U) * warps) {
-    uint4 a[U][RT][2], x[U][NT];
+  const int chunks = int(L.K / 64);
+  int c = warp;
+  for (; c + (U - 1) * warps < chunks; c += U * warps) {
+    uint4 a[U][RT][2], x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = (c + int64_t(u) * warps) * 64;
+      const int k = (c + u * warps) * 64;
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int h = 0; h < 2; ++h) a[u][r][h] = ld_stream(wp[r][h] + k);
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-        x[u][b] = xlive[b] ? __ldg(reinterpret_cast<const uint4*>(xp[b] + k)) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      x[u] = xlive ? __ldg(reinterpret_cast<const uint4*>(xp + (c + u * warps) * 64)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < U; ++u) feed(a[u], x[u]);
   }
   for (; c * 64 < L.K; c += warps) {   // fewer than U chunks left; the last one may be short
-    const int64_t k = c * 64;
+    const int k = c * 64;
     const int valid = int(min(int64_t(16), L.K - k - 16 * t));
-    uint4 a[RT][2], x[NT];
+    uint4 a[RT][2], x = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int h = 0; h < 2; ++h) a[r][h] = valid >= 16 ? ld_stream(wp[r][h] + k) : ld_part(wp[r][h] + k, valid);
-#pragma unroll
-    for (int b = 0; b < NT; ++b)
-      x[b] = !xlive[b]     ? make_uint4(0, 0, 0, 0)
-             : valid >= 16 ? __ldg(reinterpret_cast<const uint4*>(xp[b] + k))
-                           : ld_part(xp[b] + k, valid);
+    if (xlive) x = valid >= 16 ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : ld_part(xp + k, valid);
     feed(a, x);
   }
 
-  constexpr int kTok = 8 * NT;
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[((warp * RT + r) * kTok + 8 * b + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[r][b][i];
+    for (int i = 0; i < 4; ++i) red[warp][r][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[r][i];
   __syncthreads();
-  for (int o = threadIdx.x; o < kTok * 16; o += blockDim.x) {
-    const int64_t n = n0 + (o & 15), m = m0 + (o >> 4);
-    if (n >= L.N || m >= L.M) continue;
-    int s[RT] = {};
-    for (int w = 0; w < warps; ++w)
+  if (threadIdx.x < kTokens * 16) {
+    const int m = threadIdx.x >> 4, row = threadIdx.x & 15;
+    const int64_t n = n0 + row;
+    if (n < L.N && m < L.M) {
+      int s[RT] = {};
+      for (int w = 0; w < warps; ++w)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) s[r] += red[(w * RT + r) * kTok * 16 + o];
-    const float sx = L.xs[m];
-    float v = scaled(s[0], sx, L.s0[n]);
-    if constexpr (GATED) v = apply_act(v, L.act) * scaled(s[1], sx, L.s1[n]);
-    store_one(L.y, m * L.ldy + n, v, L.type);
+        for (int r = 0; r < RT; ++r) s[r] += red[w][r][m][row];
+      const float sx = L.xs[m];
+      float v = scaled(s[0], sx, L.s0[n]);
+      if constexpr (GATED) v = apply_act(v, L.act) * scaled(s[1], sx, L.s1[n]);
+      store_one(L.y, m * L.ldy + n, v, L.type);
+    }
   }
 }
 
-template <int NT, bool GATED, int U>
-cudaError_t launch_nt(const Linear& L, cudaStream_t st) {
-  const int64_t gx = (L.N + 15) / 16, gy = (L.M + 8 * NT - 1) / (8 * NT);
-  if (gx > 0x7fffffff || gy > 65535) return cudaErrorInvalidValue;
-  const int warps = 8;
-  const size_t smem = size_t(warps) * (GATED ? 2 : 1) * NT * 8 * 16 * 4;
-  gemv_i8_kernel<NT, GATED, U><<<dim3(unsigned(gx), unsigned(gy)), 32 * warps, smem, st>>>(L);
-  return cudaGetLastError();
+template <bool GATED, int U>
+cudaError_t launch_as(const Linear& L, cudaStream_t st) {
+  const int64_t tiles = (L.N + 15) / 16;
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  // four warps a CTA, more where there are so few tiles that an SM would hold
+  // under eight warps
+  int warps = 4;
+  while (warps < kMaxWarps && tiles * warps < 148 * 8) warps *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles));
+  cfg.blockDim = dim3(unsigned(32 * warps));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemv_i8_kernel<GATED, U>, L);
 }
 
 }  // namespace
 
 cudaError_t launch_gemv(const Linear& L, cudaStream_t st) {
-  const bool gated = L.act != kNone;
-  if (L.M <= 8) return gated ? launch_nt<1, true, 4>(L, st) : launch_nt<1, false, 4>(L, st);
-  return gated ? launch_nt<2, true, 2>(L, st) : launch_nt<2, false, 4>(L, st);
+  return L.act != kNone ? launch_as<true, 4>(L, st) : launch_as<false, 8>(L, st);
 }
 
 }  // namespace i8

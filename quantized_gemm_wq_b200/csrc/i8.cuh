@@ -64,6 +64,12 @@ __device__ __forceinline__ void store_one(void* y, int64_t i, float v, int type)
     static_cast<float*>(y)[i] = v;
 }
 
+// Programmatic dependent launch: the next kernel of the stream may set itself
+// up from here on; this one touches no memory of its own before the kernels
+// ahead of it are complete.
+__device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 cudaError_t launch_quantize(const void* x, int type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
                             int64_t ldc, float* scales, cudaStream_t st);
 cudaError_t launch_gemv(const Linear& L, cudaStream_t st);

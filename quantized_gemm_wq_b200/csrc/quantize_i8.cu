@@ -19,16 +19,19 @@
 //
 // The codes are exact without a division per element.  With c = fp32(1/s) the
 // product x c is within 127.5 * 2^-24 < 2^-17 of x/s; t = fma(x, c, 1.5 2^23)
-// rounds it to the nearest integer n (the code is t's low byte) and d =
-// fma(x, c, -n) is its distance from there.  Where |d| <= 1/2 - 2^-14 the
-// exact quotient rounds to the same n.  Else, about one element in ten
-// thousand, x is compared with h s, h = n + 1/2 or n - 1/2 the half it is next
-// to: fma(-h, s, x) has the exact sign (both are multiples of 2^-124 where s >=
-// 2^-100, so it cannot vanish by underflow).  Rows whose scale is below 2^-100
-// take quotients in 64 bits, which are exact enough: two 24-bit numbers'
-// quotient that is no half-integer differs from one by over 2^-33 of its size.
-// (With that division inlined for every element the kernel was bound by
-// instruction fetches: 2048 x 13824 bf16 took 63 us.)
+// rounds it to an integer n (t's low byte is the code), which is the right one
+// or its neighbour across a half.  The remainder e = fma(-n, s, x) is exact: for
+// |x| >= s it is a multiple of s's last place below 2^24 of them, for |x| in
+// [s/2, s) of half that place, below it n = 0 (or e is -s/2 .. 0).  So n is
+// right where |e| < s/2, and one too small or large where |e| > s/2; where |e| =
+// s/2 the even neighbour is.  That correction is a branch that a vector takes
+// when it holds an |e| >= s/2.  Those are not as rare as 127 * 2^-24: 16-bit
+// values have quotients 127 a/b of small integers, one in a few hundred of
+// which lies within an fp32 rounding of a half, so the branch has to be cheap
+// (a 64-bit division there took 2048 x 13824 bf16 from 20 to 63 us).
+// Scales below 2^-100, where 1/s or s's last place leave fp32's normal range,
+// take every quotient in 64 bits: of two 24-bit numbers, one that is no
+// half-integer differs from one by over 2^-33 of its size.
 #include <type_traits>
 
 #include "i8.cuh"
@@ -72,20 +75,50 @@ struct Vec {
   }
 };
 
-// VE elements from k on; elements outside 0 .. K - 1 read as 0.
+// VE elements from k on, all inside the row.
 template <int TYPE, bool ALIGNED>
-__device__ __forceinline__ uint4 load_vec(const typename Vec<TYPE>::Elem* row, int64_t k, int64_t K) {
-  constexpr int VE = Vec<TYPE>::VE;
-  if (k + VE <= K && (ALIGNED || k >= 0)) return __ldg(reinterpret_cast<const uint4*>(row + k));
+__device__ __forceinline__ uint4 load_vec(const typename Vec<TYPE>::Elem* p) {
+  if constexpr (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
+  if constexpr (TYPE == kF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(p + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = uint32_t(__ldg(p + 2 * i)) | uint32_t(__ldg(p + 2 * i + 1)) << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The first n < VE elements at p, zeros behind them.
+template <int TYPE>
+__device__ __forceinline__ uint4 load_tail(const typename Vec<TYPE>::Elem* p, int n) {
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < VE; ++i)
-    if (k + i >= 0 && k + i < K) {
-      const uint32_t e = row[k + i];
-      if constexpr (TYPE == kF32) w[i] = e;
-      else w[i >> 1] |= e << (16 * (i & 1));
+  for (int i = 0; i < Vec<TYPE>::VE; ++i)
+    if (i < n) {
+      if constexpr (TYPE == kF32) w[i] = __ldg(p + i);
+      else w[i >> 1] |= uint32_t(__ldg(p + i)) << (16 * (i & 1));
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __noinline__ uint32_t code_by_division(float x, float s) {
@@ -96,28 +129,29 @@ __device__ __noinline__ uint32_t code_by_division(float x, float s) {
 template <int TYPE>
 __device__ __forceinline__ void codes_of(const uint4& v, float s, float inv, uint32_t (&out)[2]) {
   constexpr int VE = Vec<TYPE>::VE;
+  constexpr float kMagic = 12582912.0f;   // 1.5 2^23: the unit in the last place is 1
   uint32_t b[VE];
   if (inv != 0.0f) {
-    float worst = 0.0f;
+    float e[VE], worst = 0.0f;
+    const uint64_t inv2 = f32x2(inv, inv), magic2 = f32x2(kMagic, kMagic), minus2 = f32x2(-s, -s);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float x = Vec<TYPE>::value(v, i);
-      const float t = __fmaf_rn(x, inv, 12582912.0f);   // 1.5 2^23: the unit in the last place is 1
-      b[i] = __float_as_uint(t);
-      worst = fmaxf(worst, fabsf(__fmaf_rn(x, inv, -(t - 12582912.0f))));
+    for (int i = 0; i < VE; i += 2) {
+      const uint64_t x = f32x2(Vec<TYPE>::value(v, i), Vec<TYPE>::value(v, i + 1));
+      const uint64_t t = fma2(x, inv2, magic2);
+      float t0, t1;
+      unpack2(t, t0, t1);
+      b[i] = __float_as_uint(t0);
+      b[i + 1] = __float_as_uint(t1);
+      unpack2(fma2(add2(t, f32x2(-kMagic, -kMagic)), minus2, x), e[i], e[i + 1]);
+      worst = fmaxf(worst, fmaxf(fabsf(e[i]), fabsf(e[i + 1])));
     }
-    if (worst > 0.5f - 0x1p-14f) {
+    const float half = 0.5f * s;
+    if (worst >= half) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        const float x = Vec<TYPE>::value(v, i);
-        const float n = __uint_as_float(b[i]) - 12582912.0f;
-        const float d = __fmaf_rn(x, inv, -n);
-        if (fabsf(d) > 0.5f - 0x1p-14f) {
-          const float h = n + copysignf(0.5f, d);
-          const float e = __fmaf_rn(-h, s, x);
-          // above the half, below it, or on it: h rounds to its even neighbour
-          b[i] = uint32_t(int(e > 0.0f ? h + 0.5f : e < 0.0f ? h - 0.5f : rintf(h)));
-        }
+        // past the half, or on it from an odd integer (the bits of magnitudes order as they do)
+        const uint32_t eb = __float_as_uint(e[i]);
+        if ((eb & 0x7fffffffu) + (b[i] & 1u) > __float_as_uint(half)) b[i] += uint32_t(int(eb) >> 31) | 1u;
       }
     }
   } else {
@@ -143,26 +177,28 @@ __global__ void __launch_bounds__(kThreads) quantize_i8_kernel(const void* __res
   const bool live = r < R;
   const int t0 = (warp % wpr) * 32 + lane, tn = 32 * wpr;
   const auto* row = static_cast<const typename V::Elem*>(xv) + (live ? r * ldx : 0);
-  // elements between the 16-byte boundary at or below the row's start and the
-  // row: vector j holds elements j VE - off ..
-  const int off = ALIGNED ? 0 : int((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(typename V::Elem));
-  const int64_t nvec = live ? (K + off + VE - 1) / VE : 0;
+  const int nvec = live ? int(K) / VE : 0, rest = live ? int(K) % VE : 0;   // whole vectors, elements behind them
+  pdl_start();
+  pdl_wait();
 
-  uint4 v[NV > 0 ? NV : 1];
+  uint4 v[NV > 0 ? NV : 1], tail = make_uint4(0, 0, 0, 0);
   uint32_t m = 0;
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t j = t0 + int64_t(i) * tn;
-      v[i] = j < nvec ? load_vec<TYPE, ALIGNED>(row, j * VE - off, K) : make_uint4(0, 0, 0, 0);
+      const int j = t0 + i * tn;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (j < nvec) v[i] = load_vec<TYPE, ALIGNED>(row + j * VE);
     }
+    if (t0 == 0 && rest) tail = load_tail<TYPE>(row + nvec * VE, rest);
 #pragma unroll
     for (int i = 0; i < NV; ++i) m = V::fold(m, v[i]);
   } else {
+    if (t0 == 0 && rest) tail = load_tail<TYPE>(row + nvec * VE, rest);
 #pragma unroll 4
-    for (int64_t j = t0; j < nvec; j += tn) m = V::fold(m, load_vec<TYPE, ALIGNED>(row, j * VE - off, K));
+    for (int j = t0; j < nvec; j += tn) m = V::fold(m, load_vec<TYPE, ALIGNED>(row + j * VE));
   }
-  m = V::to_f32_bits(m);
+  m = V::to_f32_bits(V::fold(m, tail));
   m = __reduce_max_sync(0xffffffffu, m);
   if (wpr > 1) {
     if (lane == 0) smax[warp] = m;
@@ -178,28 +214,26 @@ __global__ void __launch_bounds__(kThreads) quantize_i8_kernel(const void* __res
   const bool zero = !finite || s == 0.0f;
   const float inv = s >= 0x1p-100f && finite ? __fdiv_rn(1.0f, s) : 0.0f;
   int8_t* out = codes + r * ldc;
-  auto put = [&](int64_t j, const uint4& x) {
+  auto put = [&](int j, const uint4& x) {
     uint32_t c[2] = {0u, 0u};
     if (!zero) codes_of<TYPE>(x, s, inv, c);
-    const int64_t k = j * VE - off;
-    if (ALIGNED && k + VE <= K) {
-      if constexpr (VE == 8) *reinterpret_cast<uint2*>(out + k) = make_uint2(c[0], c[1]);
-      else *reinterpret_cast<uint32_t*>(out + k) = c[0];
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (k + i >= 0 && k + i < K) out[k + i] = int8_t(c[i / 4] >> (8 * (i & 3)));
-    }
+    if constexpr (VE == 8) *reinterpret_cast<uint2*>(out + j * VE) = make_uint2(c[0], c[1]);
+    else *reinterpret_cast<uint32_t*>(out + j * VE) = c[0];
   };
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t j = t0 + int64_t(i) * tn;
+      const int j = t0 + i * tn;
       if (j < nvec) put(j, v[i]);
     }
   } else {
 #pragma unroll 2
-    for (int64_t j = t0; j < nvec; j += tn) put(j, load_vec<TYPE, ALIGNED>(row, j * VE - off, K));
+    for (int j = t0; j < nvec; j += tn) put(j, load_vec<TYPE, ALIGNED>(row + j * VE));
+  }
+  if (t0 == 0 && rest) {
+    uint32_t c[2] = {0u, 0u};
+    if (!zero) codes_of<TYPE>(tail, s, inv, c);
+    for (int i = 0; i < rest; ++i) out[nvec * VE + i] = int8_t(c[i / 4] >> (8 * (i & 3)));
   }
 }
 
@@ -207,7 +241,7 @@ template <int TYPE, bool ALIGNED>
 cudaError_t launch_typed(const void* x, int64_t R, int64_t K, int64_t ldx, int8_t* codes, int64_t ldc, float* scales,
                          cudaStream_t st) {
   constexpr int VE = Vec<TYPE>::VE;
-  const int64_t nvec = (K + (ALIGNED ? 0 : VE - 1) + VE - 1) / VE;   // the most that a row can span
+  const int64_t nvec = K / VE;
   // warps per row: two vectors a thread and more before the next warp joins
   // in, and all eight when there are few rows
   int wpr = 1;
@@ -215,18 +249,21 @@ cudaError_t launch_typed(const void* x, int64_t R, int64_t K, int64_t ldx, int8_
   const int64_t per = (nvec + 32 * wpr - 1) / (32 * wpr);
   const int64_t grid = (R + 8 / wpr - 1) / (8 / wpr);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 g{unsigned(grid)}, b{kThreads};
-  if (per <= 1)
-    quantize_i8_kernel<TYPE, 1, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
-  else if (per <= 2)
-    quantize_i8_kernel<TYPE, 2, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
-  else if (per <= 4)
-    quantize_i8_kernel<TYPE, 4, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
-  else if (per <= 8)
-    quantize_i8_kernel<TYPE, 8, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
-  else
-    quantize_i8_kernel<TYPE, 0, ALIGNED><<<g, b, 0, st>>>(x, R, K, ldx, codes, ldc, scales, wpr);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* fn = per <= 1   ? quantize_i8_kernel<TYPE, 1, ALIGNED>
+             : per <= 2 ? quantize_i8_kernel<TYPE, 2, ALIGNED>
+             : per <= 4 ? quantize_i8_kernel<TYPE, 4, ALIGNED>
+             : per <= 8 ? quantize_i8_kernel<TYPE, 8, ALIGNED>
+                        : quantize_i8_kernel<TYPE, 0, ALIGNED>;
+  return cudaLaunchKernelEx(&cfg, fn, x, R, K, ldx, codes, ldc, scales, wpr);
 }
 
 template <int TYPE>
