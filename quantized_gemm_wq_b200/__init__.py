@@ -264,36 +264,44 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # wq_type
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}                        # wq_act
 
 
+def _current_raw_stream(index: int) -> int:
+    # torch.cuda.current_stream() builds a Stream object, 3 us of a call that takes 8
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+
 def _rows(t: torch.Tensor, what: str) -> int:
     """Row stride of a 2-D CUDA tensor whose columns are adjacent."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    ld, step = t.stride()
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{what} must have adjacent columns (stride 1)")
     # the stride of a single row is never taken: any valid one will do
-    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    return ld if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _codes(t: torch.Tensor, what: str) -> int:
-    if t.dtype != torch.int8:
+    if t.dtype is not torch.int8:
         raise ValueError(f"{what} must be int8 codes")
     return _rows(t, what)
 
 
 def _scales(t: torch.Tensor, n: int, dev, what: str) -> int:
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != dev or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.shape != (n,) or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous fp32 [{n}] tensor on the codes' device")
     return t.data_ptr()
 
 
 def _call(fn, where: str, dev, stream, *args) -> None:
     """fn(*args, stream) with `dev` current: its current stream when `stream` is None."""
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, _current_raw_stream(i) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+            st = fn(*args, _current_raw_stream(i) if stream is None else stream.cuda_stream)
     if st != WQ_OK:
         raise WQError(st, where)
 
@@ -302,12 +310,11 @@ def _output(y, M: int, N: int, dtype, dev, what: str):
     if y is None:
         if dtype not in _TYPES:
             raise ValueError("dtype must be torch.bfloat16, torch.float16 or torch.float32")
-        y = torch.empty((M, N), dtype=dtype, device=dev)
-        return y, N
-    if y.dtype not in _TYPES or tuple(y.shape) != (M, N) or y.device != dev:
+        return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=dev), N, _TYPES[dtype]
+    if y.dtype not in _TYPES or y.shape != (M, N) or y.device != dev:
         raise ValueError(f"{what} must be a bf16, fp16 or fp32 [{M}, {N}] tensor on the codes' device")
     ld = _rows(y, what)
-    return y, ld if M > 1 else max(ld, N)
+    return y, ld if M > 1 else max(ld, N), _TYPES[y.dtype]
 
 
 def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
@@ -315,27 +322,25 @@ def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     -> (int8 codes [R, K], fp32 scales [R]), ``x ~ codes * scales[:, None]``.
     The codes' rows start at multiples of 16 bytes: for other K the returned
     tensor is a view of a wider one."""
-    if x.dtype not in _TYPES:
+    xt = _TYPES.get(x.dtype)
+    if xt is None:
         raise ValueError("x must be bf16, fp16 or fp32")
     ldx = _rows(x, "x")
     R, K = x.shape
     dev = x.device
     if codes is None:
         ldc = (K + 15) // 16 * 16
-        codes = torch.empty((R, ldc), dtype=torch.int8, device=dev)
-        if ldc != K:
-            codes = codes[:, :K]
+        codes = torch.empty_strided((R, K), (ldc, 1), dtype=torch.int8, device=dev)
     else:
         ldc = _codes(codes, "codes")
         if codes.shape != x.shape or codes.device != dev:
             raise ValueError("codes must have x's shape and device")
     if scales is None:
-        scales = torch.empty((R,), dtype=torch.float32, device=dev)
+        scales = torch.empty_strided((R,), (1,), dtype=torch.float32, device=dev)
         sp = scales.data_ptr()
     else:
         sp = _scales(scales, R, dev, "scales")
-    _call(lib.wq_quantize_i8, "wq_quantize_i8", dev, stream, x.data_ptr(), _TYPES[x.dtype], R, K, ldx,
-          codes.data_ptr(), ldc, sp)
+    _call(lib.wq_quantize_i8, "wq_quantize_i8", dev, stream, x.data_ptr(), xt, R, K, ldx, codes.data_ptr(), ldc, sp)
     return codes, scales
 
 
@@ -351,9 +356,9 @@ def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     if Kw != K or w.device != dev:
         raise ValueError("w must be [N, K] with x's K, on x's device")
     xs, ws = _scales(x_scales, M, dev, "x_scales"), _scales(w_scales, N, dev, "w_scales")
-    y, ldy = _output(y, M, N, dtype, dev, "y")
+    y, ldy, yt = _output(y, M, N, dtype, dev, "y")
     _call(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w.data_ptr(), ldw, ws,
-          y.data_ptr(), _TYPES[y.dtype], ldy)
+          y.data_ptr(), yt, ldy)
     return y
 
 
@@ -373,7 +378,7 @@ def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, g
         raise ValueError("w_gate and w_up must be [N, K] with x's K and one row stride, on x's device")
     xs = _scales(x_scales, M, dev, "x_scales")
     gs, us = _scales(gate_scales, N, dev, "gate_scales"), _scales(up_scales, N, dev, "up_scales")
-    h, ldh = _output(h, M, N, dtype, dev, "h")
+    h, ldh, ht = _output(h, M, N, dtype, dev, "h")
     _call(lib.wq_gated_i8, "wq_gated_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w_gate.data_ptr(), gs,
-          w_up.data_ptr(), us, ldw, _ACTS[act], h.data_ptr(), _TYPES[h.dtype], ldh)
+          w_up.data_ptr(), us, ldw, _ACTS[act], h.data_ptr(), ht, ldh)
     return h
