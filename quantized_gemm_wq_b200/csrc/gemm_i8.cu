@@ -111,6 +111,9 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* m, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(m), "r"(c0), "r"(c1) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
@@ -228,6 +231,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   if (ks > 1) cluster_arrive();        // waited for before the first write to a peer: it runs by then
+  // The first weight tiles on their way to L2 while the kernel ahead finishes:
+  // only L2, which sees whatever that kernel may yet write to them.
+  if (warp == 0 && elect_one())
+    for (int i = 0; i < min(S, nkb); ++i) {
+      prefetch_tile(&p.t0, (kb0 + i) * kBK, int(n0));
+      if constexpr (GATED) prefetch_tile(&p.t1, (kb0 + i) * kBK, int(n0));
+    }
+  __syncwarp();
   pdl_wait();
 
   // Warps 0 and 1 stay whole, so that what they compute for the one issuing
@@ -388,14 +399,22 @@ __device__ __forceinline__ void flush_rows(const uint8_t* out, const Linear& L, 
             *reinterpret_cast<const uint4*>(out + row * kOutRow + at);
     }
   } else {
-    const int col = lane & (cols - 1), per = 32 / cols;
-    if (n + col < L.N)
-      for (int row = lane / cols; row < 32 && m + row < L.M; row += per) {
-        const uint8_t* src = out + row * kOutRow + col * eb;
-        uint8_t* dst = y + ((m + row) * L.ldy + n + col) * eb;
-        if (eb == 4) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
-        else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+    const int col = lane & (cols - 1), per = 32 / cols, first = lane / cols;
+    if (n + col < L.N) {
+      const int rows = int(min(int64_t(32), L.M - m));
+      const uint8_t* src = out + first * kOutRow + col * eb;
+      uint8_t* dst = y + ((m + first) * L.ldy + n + col) * eb;
+      const int64_t hop = per * L.ldy * eb;
+      if (eb == 4) {
+#pragma unroll 8
+        for (int row = first; row < rows; row += 2, src += 2 * kOutRow, dst += hop)
+          *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+      } else {
+#pragma unroll 8
+        for (int row = 0; row < rows; ++row, src += kOutRow, dst += hop)
+          *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
       }
+    }
   }
   __syncwarp();
 }

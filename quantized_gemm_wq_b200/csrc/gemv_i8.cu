@@ -5,13 +5,13 @@
 // s32), the tokens its N side, so up to 8 tokens cost one MMA per 512 weights.
 // A sum over k may be taken in any order, so both operands are loaded 16 bytes
 // a lane from the same places of their rows and the MMA's k index is renamed:
-// lane (g, t) holds bytes 16 t .. 16 t + 15 of a 64-byte chunk of rows g and
-// g + 8 and of token g, which are the A and B fragments of two MMAs.  Weights
-// go straight from memory to registers; nothing is staged.
+// lane (g, t) holds bytes 16 t .. 16 t + 15 of a 64-byte half chunk of rows g
+// and g + 8 and of token g, which are the A and B fragments of two MMAs.
+// Weights go straight from memory to registers; nothing is staged.
 //
 // One CTA computes 16 output rows (of both projections in a gated call) for
-// all tokens; its warps take the 64-byte chunks of K in turn, several chunks'
-// loads in flight each, and their int32 sums meet in shared memory.
+// all tokens; its warps take the 128-byte chunks of K in turn, the next
+// chunks' loads in flight while the present ones are multiplied, and their int32 sums meet in shared memory.
 #include "i8.cuh"
 #include "wq_internal.cuh"
 
@@ -38,6 +38,7 @@ __device__ __forceinline__ uint4 ld_stream(const int8_t* p) {
                : "l"(p));
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // The first `valid` (< 16) bytes at p, zeros behind them.
 __device__ __forceinline__ uint4 ld_part(const int8_t* p, int valid) {
   uint32_t w[4] = {0, 0, 0, 0};
@@ -47,7 +48,13 @@ __device__ __forceinline__ uint4 ld_part(const int8_t* p, int valid) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// U: chunks in flight per warp.
+// One 128-byte chunk of 16 rows (of each of RT matrices) and of the tokens.
+template <int RT>
+struct Chunk {
+  uint4 a[2][RT][2], x[2];
+};
+
+// U: chunks a warp loads at a time.
 template <bool GATED, int U>
 __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L) {
   constexpr int RT = GATED ? 2 : 1;    // tiles of 16 rows: the gate's and the up projection's
@@ -67,6 +74,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L)
   const bool xlive = g < L.M;
   const int8_t* xp = L.x + (xlive ? g : 0) * L.ldx + 16 * t;
   int acc[RT][4] = {};
+  auto load = [&](Chunk<RT> (&c)[U], int at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = (at + u * warps) * 128 + 64 * i;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) c[u].a[i][r][h] = ld_stream(wp[r][h] + k);
+        c[u].x[i] = xlive ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : make_uint4(0, 0, 0, 0);
+      }
+  };
   auto feed = [&](const uint4 (&a)[RT][2], const uint4& x) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -74,37 +94,56 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L)
       mma_s8(acc[r], a[r][0].z, a[r][1].z, a[r][0].w, a[r][1].w, x.z, x.w);
     }
   };
-  pdl_wait();
-
-  const int chunks = int(L.K / 64);
-  int c = warp;
-  for (; c + (U - 1) * warps < chunks; c += U * warps) {
-    uint4 a[U][RT][2], x[U];
+  auto feed_all = [&](const Chunk<RT> (&c)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = (c + u * warps) * 64;
+      feed(c[u].a[0], c[u].x[0]);
+      feed(c[u].a[1], c[u].x[1]);
+    }
+  };
+  const int chunks = int(L.K / 128), step = U * warps;
+  int c = warp;
+  // The first chunks of the weights on their way to L2 while the kernel ahead
+  // finishes: only L2, which sees whatever that kernel may yet write to them.
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (t == 0 && c + u * warps < chunks) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a[u][r][h] = ld_stream(wp[r][h] + k);
+        for (int h = 0; h < 2; ++h) prefetch_l2(wp[r][h] + (c + u * warps) * 128);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      x[u] = xlive ? __ldg(reinterpret_cast<const uint4*>(xp + (c + u * warps) * 64)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) feed(a[u], x[u]);
+  pdl_wait();
+
+  if (c + (U - 1) * warps < chunks) {
+    Chunk<RT> p[U], q[U];
+    load(p, c);
+    for (;;) {
+      c += step;
+      bool more = c + (U - 1) * warps < chunks;
+      if (more) load(q, c);
+      feed_all(p);
+      if (!more) break;
+      c += step;
+      more = c + (U - 1) * warps < chunks;
+      if (more) load(p, c);
+      feed_all(q);
+      if (!more) break;
+    }
   }
-  for (; c * 64 < L.K; c += warps) {   // fewer than U chunks left; the last one may be short
-    const int k = c * 64;
-    const int valid = int(min(int64_t(16), L.K - k - 16 * t));
-    uint4 a[RT][2], x = make_uint4(0, 0, 0, 0);
+  for (; c * 128 < L.K; c += warps)      // fewer than U chunks left; the last one may be short
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int i = 0; i < 2; ++i) {
+      const int k = c * 128 + 64 * i;
+      const int valid = int(min(int64_t(16), L.K - k - 16 * t));
+      uint4 a[RT][2], x = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) a[r][h] = valid >= 16 ? ld_stream(wp[r][h] + k) : ld_part(wp[r][h] + k, valid);
-    if (xlive) x = valid >= 16 ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : ld_part(xp + k, valid);
-    feed(a, x);
-  }
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[r][h] = valid >= 16 ? ld_stream(wp[r][h] + k) : ld_part(wp[r][h] + k, valid);
+      if (xlive) x = valid >= 16 ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : ld_part(xp + k, valid);
+      feed(a, x);
+    }
 
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -131,10 +170,9 @@ template <bool GATED, int U>
 cudaError_t launch_as(const Linear& L, cudaStream_t st) {
   const int64_t tiles = (L.N + 15) / 16;
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  // four warps a CTA, more where there are so few tiles that an SM would hold
-  // under eight warps
-  int warps = 4;
-  while (warps < kMaxWarps && tiles * warps < 148 * 8) warps *= 2;
+  // Eight warps a CTA; sixteen where there are fewer tiles than SMs (1024 rows,
+  // K = 8192: 4.2 against 5.6 us; 11008 rows, K = 4096: 14.0 against 10.1).
+  const int warps = tiles < 148 ? 16 : 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles));
   cfg.blockDim = dim3(unsigned(32 * warps));
@@ -150,7 +188,7 @@ cudaError_t launch_as(const Linear& L, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_gemv(const Linear& L, cudaStream_t st) {
-  return L.act != kNone ? launch_as<true, 4>(L, st) : launch_as<false, 8>(L, st);
+  return L.act != kNone ? launch_as<true, 1>(L, st) : launch_as<false, 2>(L, st);
 }
 
 }  // namespace i8
