@@ -264,57 +264,60 @@ _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # wq_type
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}                        # wq_act
 
 
-def _current_raw_stream(index: int) -> int:
-    # torch.cuda.current_stream() builds a Stream object, 3 us of a call that takes 8
-    return torch._C._cuda_getCurrentRawStream(index)
+# The three calls below are made once per layer and token, so what they do on
+# the host is kept short: device indexes instead of device objects, and the
+# current stream's address without a Stream object (3 us by itself).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_INT8, _FP32 = torch.int8, torch.float32
 
 
-
-def _rows(t: torch.Tensor, what: str) -> int:
-    """Row stride of a 2-D CUDA tensor whose columns are adjacent."""
+def _rows(t: torch.Tensor, what: str):
+    """(rows, columns, row stride) of a 2-D CUDA tensor whose columns are adjacent."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    ld, step = t.stride()
     rows, cols = t.shape
+    ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what} must have adjacent columns (stride 1)")
     # the stride of a single row is never taken: any valid one will do
-    return ld if rows > 1 else (cols + 15) // 16 * 16
+    return rows, cols, ld if rows > 1 else (cols + 15) // 16 * 16
 
 
-def _codes(t: torch.Tensor, what: str) -> int:
-    if t.dtype is not torch.int8:
+def _codes(t: torch.Tensor, what: str):
+    if t.dtype is not _INT8:
         raise ValueError(f"{what} must be int8 codes")
     return _rows(t, what)
 
 
-def _scales(t: torch.Tensor, n: int, dev, what: str) -> int:
-    if t.dtype is not torch.float32 or t.shape != (n,) or t.device != dev or not t.is_contiguous():
+def _scales(t: torch.Tensor, n: int, dev: int, what: str) -> int:
+    if t.dtype is not _FP32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous fp32 [{n}] tensor on the codes' device")
     return t.data_ptr()
 
 
-def _call(fn, where: str, dev, stream, *args) -> None:
+def _call(fn, where: str, dev: int, stream, *args) -> None:
     """fn(*args, stream) with `dev` current: its current stream when `stream` is None."""
-    i = dev.index
-    if i == torch.cuda.current_device():
-        st = fn(*args, _current_raw_stream(i) if stream is None else stream.cuda_stream)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _current_raw_stream(i) if stream is None else stream.cuda_stream)
+            st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != WQ_OK:
         raise WQError(st, where)
 
 
-def _output(y, M: int, N: int, dtype, dev, what: str):
+def _output(y, M: int, N: int, dtype, x, what: str):
+    """The output (made on x's device if None), its row stride and its wq_type."""
     if y is None:
-        if dtype not in _TYPES:
+        yt = _TYPES.get(dtype)
+        if yt is None:
             raise ValueError("dtype must be torch.bfloat16, torch.float16 or torch.float32")
-        return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=dev), N, _TYPES[dtype]
-    if y.dtype not in _TYPES or y.shape != (M, N) or y.device != dev:
+        return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=x.device), N, yt
+    yt = _TYPES.get(y.dtype)
+    if yt is None or y.shape != (M, N) or y.get_device() != x.get_device():
         raise ValueError(f"{what} must be a bf16, fp16 or fp32 [{M}, {N}] tensor on the codes' device")
-    ld = _rows(y, what)
-    return y, ld if M > 1 else max(ld, N), _TYPES[y.dtype]
+    ld = _rows(y, what)[2]
+    return y, ld if M > 1 else max(ld, N), yt
 
 
 def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
@@ -325,18 +328,17 @@ def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     xt = _TYPES.get(x.dtype)
     if xt is None:
         raise ValueError("x must be bf16, fp16 or fp32")
-    ldx = _rows(x, "x")
-    R, K = x.shape
-    dev = x.device
+    R, K, ldx = _rows(x, "x")
+    dev = x.get_device()
     if codes is None:
         ldc = (K + 15) // 16 * 16
-        codes = torch.empty_strided((R, K), (ldc, 1), dtype=torch.int8, device=dev)
+        codes = torch.empty_strided((R, K), (ldc, 1), dtype=_INT8, device=x.device)
     else:
-        ldc = _codes(codes, "codes")
-        if codes.shape != x.shape or codes.device != dev:
+        ldc = _codes(codes, "codes")[2]
+        if codes.shape != x.shape or codes.get_device() != dev:
             raise ValueError("codes must have x's shape and device")
     if scales is None:
-        scales = torch.empty_strided((R,), (1,), dtype=torch.float32, device=dev)
+        scales = torch.empty_strided((R,), (1,), dtype=_FP32, device=x.device)
         sp = scales.data_ptr()
     else:
         sp = _scales(scales, R, dev, "scales")
@@ -349,14 +351,13 @@ def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     """``y[m, n] = x_scales[m] * w_scales[n] * sum_k x[m, k] w[n, k]`` for int8
     codes ``x`` [M, K] and ``w`` [N, K] -> ``y`` [M, N] of ``dtype`` (or the
     given ``y``'s type).  Row strides of codes are multiples of 16."""
-    ldx, ldw = _codes(x, "x"), _codes(w, "w")
-    M, K = x.shape
-    N, Kw = w.shape
-    dev = x.device
-    if Kw != K or w.device != dev:
+    M, K, ldx = _codes(x, "x")
+    N, Kw, ldw = _codes(w, "w")
+    dev = x.get_device()
+    if Kw != K or w.get_device() != dev:
         raise ValueError("w must be [N, K] with x's K, on x's device")
     xs, ws = _scales(x_scales, M, dev, "x_scales"), _scales(w_scales, N, dev, "w_scales")
-    y, ldy, yt = _output(y, M, N, dtype, dev, "y")
+    y, ldy, yt = _output(y, M, N, dtype, x, "y")
     _call(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w.data_ptr(), ldw, ws,
           y.data_ptr(), yt, ldy)
     return y
@@ -368,17 +369,17 @@ def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, g
     """``h = act(x . w_gate^T) * (x . w_up^T)`` on int8 codes, both products
     scaled as in ``wq_gemm_i8``, in one kernel; ``act``: "silu", "gelu" (erf)
     or "gelu_tanh"."""
-    if act not in _ACTS:
+    at = _ACTS.get(act)
+    if at is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    ldx, ldw, ldu = _codes(x, "x"), _codes(w_gate, "w_gate"), _codes(w_up, "w_up")
-    M, K = x.shape
-    N, Kw = w_gate.shape
-    dev = x.device
-    if Kw != K or w_gate.device != dev or w_up.shape != w_gate.shape or w_up.device != dev or ldu != ldw:
+    M, K, ldx = _codes(x, "x")
+    N, Kw, ldw = gate = _codes(w_gate, "w_gate")
+    dev = x.get_device()
+    if Kw != K or _codes(w_up, "w_up") != gate or w_gate.get_device() != dev or w_up.get_device() != dev:
         raise ValueError("w_gate and w_up must be [N, K] with x's K and one row stride, on x's device")
     xs = _scales(x_scales, M, dev, "x_scales")
     gs, us = _scales(gate_scales, N, dev, "gate_scales"), _scales(up_scales, N, dev, "up_scales")
-    h, ldh, ht = _output(h, M, N, dtype, dev, "h")
+    h, ldh, ht = _output(h, M, N, dtype, x, "h")
     _call(lib.wq_gated_i8, "wq_gated_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w_gate.data_ptr(), gs,
-          w_up.data_ptr(), us, ldw, _ACTS[act], h.data_ptr(), ht, ldh)
+          w_up.data_ptr(), us, ldw, at, h.data_ptr(), ht, ldh)
     return h

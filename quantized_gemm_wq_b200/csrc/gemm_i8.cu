@@ -377,7 +377,8 @@ struct alignas(64) PairArgs {
 };
 
 constexpr int kPairThreads = 320;       // producer, MMA, eight epilogue warps
-constexpr int kPairStages = 6;
+constexpr int kPairRing = 6 * 2 * int(kTile);   // six stages of the largest tile, more of smaller ones
+constexpr int kPairStages = 9;
 constexpr int kGroupM = 16;             // token tiles that neighbouring tiles walk through first
 
 // A warp's 32 rows of 64 output bytes, from its staging buffer to columns n ..
@@ -685,7 +686,7 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   p.mt = int(L.M >= kSplitTokens ? kSplitTokens : (L.M + 31) / 32 * 32);
   constexpr int kOut = GATED ? 64 : 128;
   if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, kOut) ||
-      !make_map(&p.t1, GATED ? L.w1 : L.w0, L.K, L.N, L.ldw, kOut))
+      (GATED && !make_map(&p.t1, L.w1, L.K, L.N, L.ldw, kOut)))
     return cudaErrorInvalidValue;
   const int eb = type_bytes(L.type);
   p.vec = reinterpret_cast<uintptr_t>(L.y) % (4 * eb) == 0 && (L.ldy * eb) % (4 * eb) == 0;
@@ -723,7 +724,7 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
   cudaError_t e = current_device(&dev);
   if (e != cudaSuccess) return e;
   static std::atomic<bool> set[64];
-  if ((e = allow_smem(gemm_i8_pair_kernel<GATED>, kPairStages * 2 * kTile + 1024, set, dev)) != cudaSuccess) return e;
+  if ((e = allow_smem(gemm_i8_pair_kernel<GATED>, kPairRing + 1024, set, dev)) != cudaSuccess) return e;
   const int pairs = sm_count(dev) / 2;
   PairArgs p;
   p.L = L;
@@ -744,12 +745,13 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
   p.tiles_m = int(tm);
   p.tiles_n = int(tn);
   if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, 128) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, p.bn / 2) ||
-      !make_map(&p.t1, GATED ? L.w1 : L.w0, L.K, L.N, L.ldw, p.bn / 2))
+      (GATED && !make_map(&p.t1, L.w1, L.K, L.N, L.ldw, p.bn / 2)))
     return cudaErrorInvalidValue;
   const int eb = type_bytes(L.type);
   p.vec = reinterpret_cast<uintptr_t>(L.y) % 16 == 0 && (L.ldy * eb) % 16 == 0;
   const uint32_t stage = kTile + uint32_t(p.bn / 2) * kBK;
-  p.stages = kPairStages;
+  p.stages = kPairRing / int(stage);
+  if (p.stages > kPairStages) p.stages = kPairStages;
   const int64_t ctas = 2 * (tm * tn < pairs ? tm * tn : pairs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
