@@ -306,13 +306,23 @@ def _call(fn, where: str, dev: int, stream, *args) -> None:
         raise WQError(st, where)
 
 
-def _output(y, M: int, N: int, dtype, x, what: str):
+def _empty(size, strides, dtype, x, stream):
+    """Uninitialised memory on x's device, of the stream that will write it."""
+    if stream is None:
+        return torch.empty_strided(size, strides, dtype=dtype, device=x.device)
+    if stream.device != x.device:
+        raise ValueError("stream must be one of the operands' device")
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(size, strides, dtype=dtype, device=x.device)
+
+
+def _output(y, M: int, N: int, dtype, x, stream, what: str):
     """The output (made on x's device if None), its row stride and its wq_type."""
     if y is None:
         yt = _TYPES.get(dtype)
         if yt is None:
             raise ValueError("dtype must be torch.bfloat16, torch.float16 or torch.float32")
-        return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=x.device), N, yt
+        return _empty((M, N), (N, 1), dtype, x, stream), N, yt
     yt = _TYPES.get(y.dtype)
     if yt is None or y.shape != (M, N) or y.get_device() != x.get_device():
         raise ValueError(f"{what} must be a bf16, fp16 or fp32 [{M}, {N}] tensor on the codes' device")
@@ -323,22 +333,25 @@ def _output(y, M: int, N: int, dtype, x, what: str):
 def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     """Quantise every row of bf16/fp16/fp32 ``x`` [R, K] (CUDA, any row stride)
     -> (int8 codes [R, K], fp32 scales [R]), ``x ~ codes * scales[:, None]``.
-    The codes' rows start at multiples of 16 bytes: for other K the returned
-    tensor is a view of a wider one."""
+    The codes' rows start at multiples of 16 bytes (128 for K > 1024), so for
+    other K they do not lie side by side."""
     xt = _TYPES.get(x.dtype)
     if xt is None:
         raise ValueError("x must be bf16, fp16 or fp32")
     R, K, ldx = _rows(x, "x")
     dev = x.get_device()
     if codes is None:
-        ldc = (K + 15) // 16 * 16
-        codes = torch.empty_strided((R, K), (ldc, 1), dtype=_INT8, device=x.device)
+        # whole 128-byte lines a row where that costs little: the tensor-core
+        # kernels fetch rows in pieces of 128 bytes (333 x 5003 -> 4992: 17.4 us
+        # with rows of 5008 bytes, 13.7 with 5120)
+        ldc = (K + 127) // 128 * 128 if K > 1024 else (K + 15) // 16 * 16
+        codes = _empty((R, K), (ldc, 1), _INT8, x, stream)
     else:
         ldc = _codes(codes, "codes")[2]
         if codes.shape != x.shape or codes.get_device() != dev:
             raise ValueError("codes must have x's shape and device")
     if scales is None:
-        scales = torch.empty_strided((R,), (1,), dtype=_FP32, device=x.device)
+        scales = _empty((R,), (1,), _FP32, x, stream)
         sp = scales.data_ptr()
     else:
         sp = _scales(scales, R, dev, "scales")
@@ -357,7 +370,7 @@ def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     if Kw != K or w.get_device() != dev:
         raise ValueError("w must be [N, K] with x's K, on x's device")
     xs, ws = _scales(x_scales, M, dev, "x_scales"), _scales(w_scales, N, dev, "w_scales")
-    y, ldy, yt = _output(y, M, N, dtype, x, "y")
+    y, ldy, yt = _output(y, M, N, dtype, x, stream, "y")
     _call(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w.data_ptr(), ldw, ws,
           y.data_ptr(), yt, ldy)
     return y
@@ -379,7 +392,7 @@ def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, g
         raise ValueError("w_gate and w_up must be [N, K] with x's K and one row stride, on x's device")
     xs = _scales(x_scales, M, dev, "x_scales")
     gs, us = _scales(gate_scales, N, dev, "gate_scales"), _scales(up_scales, N, dev, "up_scales")
-    h, ldh, ht = _output(h, M, N, dtype, x, "h")
+    h, ldh, ht = _output(h, M, N, dtype, x, stream, "h")
     _call(lib.wq_gated_i8, "wq_gated_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w_gate.data_ptr(), gs,
           w_up.data_ptr(), us, ldw, at, h.data_ptr(), ht, ldh)
     return h
