@@ -679,6 +679,34 @@ cudaError_t current_device(int* dev) {
   return *dev >= 0 && *dev < 64 ? cudaSuccess : cudaErrorInvalidDevice;
 }
 
+// How many clusters of ks CTAs of the split kernel, one CTA an SM, run at once:
+// fewer than the SMs divided by ks, as a cluster stays within one group of SMs
+// (16 clusters of 8 took two rounds: 14.0 us against 9.1 over 4).
+template <bool GATED>
+int clusters_at_once(int dev, int ks) {
+  static std::atomic<int> cached[64][kSplitMax + 1];
+  int n = cached[dev][ks].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, unsigned(ks));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = kSmemMax - 4096;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = unsigned(ks);
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_i8_split_kernel<GATED>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = 1;
+    }
+    cached[dev][ks].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 template <bool GATED>
 cudaError_t split(const Linear& L, cudaStream_t st) {
   int dev;
@@ -699,11 +727,11 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   const uint32_t stage = kTile + uint32_t(p.mt) * kBK;
   const int64_t tiles = (L.N + kOut - 1) / kOut, kb = (L.K + kBK - 1) / kBK;
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  // Split K while every CTA still gets an SM of its own (64 tokens, 4096 x 4096,
-  // 32 tiles: 11.0 us unsplit, 9.0 / 8.4 / 9.1 over 2 / 4 / 8 CTAs; 11008 x 4096,
-  // 86 tiles: 12.9 unsplit, 14.2 over 2).
+  // Split K while all clusters are on the SMs at once, one CTA an SM (64 tokens,
+  // 4096 x 4096, 32 tiles: 11.0 us unsplit, 9.0 / 8.4 / 9.1 over 2 / 4 / 8
+  // CTAs; 11008 x 4096, 86 tiles: 12.9 unsplit, 14.2 over 2).
   int ks = 1;
-  while (ks < kSplitMax && tiles * ks * 2 <= nsm && kb >= 4 * ks) ks *= 2;
+  while (ks < kSplitMax && kb >= 4 * ks && tiles <= clusters_at_once<GATED>(dev, 2 * ks)) ks *= 2;
   const uint32_t parked = ks > 1 ? uint32_t(p.mt) * 512 : 0;
   // two CTAs an SM where there are more than SMs, else one with a deeper ring
   const uint32_t budget = (tiles * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
