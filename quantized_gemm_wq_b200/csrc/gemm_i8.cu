@@ -243,13 +243,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
 
   // Warps 0 and 1 stay whole, so that what they compute for the one issuing
   // lane lives in uniform registers, where the TMA and MMA instructions read it.
+  int issued = 0;                      // stages that warp 0 has asked for
   if (warp == 0) {
-    int issued = 0;
-    bool ok = true;
     Slot at;
     for (int i = 0; i < nkb; ++i, at.next(S)) {
-      if (i >= S) ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort));
-      if (!ok) break;
+      if (i >= S && !__all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort))) break;
       uint8_t* w = ring + at.s * stage;
       const int k = (kb0 + i) * kBK;
       if (elect_one()) {
@@ -260,9 +258,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
       }
       ++issued;
     }
-    if (!ok && lane == 0)   // copies in flight land before shared memory goes away
-      for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-        mbar_drain(&full[i % S], (i / S) & 1, &g_gemm_i8_timeout);
   } else if (warp == 1) {
     const uint32_t idesc = i8_idesc(128, mt);
     const uint64_t ring_desc = sw128_desc(smem_u32(ring));
@@ -354,11 +349,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   }
   tc_fence_before();
   __syncthreads();
+  // Given up: the copies in flight land before shared memory goes away, the
+  // MMAs issued end before tensor memory does.
+  if (*abort && lane == 0) {
+    if (warp == 0)
+      for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+        mbar_drain(&full[i % S], (i / S) & 1, &g_gemm_i8_timeout);
+    if (warp == 1) mbar_drain(&done, 0, &g_gemm_i8_timeout);
+  }
+  __syncwarp();
   if (warp == 1) {
-    if (*abort) {
-      if (lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
-      __syncwarp();
-    }
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
   }
@@ -484,10 +484,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   // Warps 0 and 1 stay whole, so that what they compute for the one issuing
   // lane lives in uniform registers, where the TMA and MMA instructions read it
   // (with a lone lane the MMA warp needed over 600 cycles a stage of 512).
+  int64_t issued = 0;                  // stages that warp 0 has asked for
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    int i = 0;
     Slot at;
     const uint32_t full0 = mapa(smem_u32(&full[0]), 0);      // the leader's barriers
     const CUtensorMap* tw = GATED && rank == 1 ? &p.t1 : &p.t0;
@@ -496,8 +496,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
       const int mrow = tm * 256 + int(rank) * 128;
       const int nrow = GATED ? tn * out_n : tn * bn + int(rank) * (bn / 2);
-      for (int kb = 0; kb < nkb; ++kb, ++i, at.next(S)) {
-        if (i >= S) ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort));
+      for (int kb = 0; kb < nkb; ++kb, ++issued, at.next(S)) {
+        if (issued >= S) ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort));
         if (!ok) break;
         uint8_t* a = ring + at.s * stage;
         const uint32_t bar = full0 + uint32_t(at.s) * 8;
@@ -506,18 +506,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tma_load_pair(a, &p.tx, bar, kb * kBK, mrow);
           tma_load_pair(a + kTile, tw, bar, kb * kBK, nrow);
         }
-      }
-    }
-    // Given up: what is in flight lands before shared memory goes away.  The
-    // leader's barriers count both CTAs' bytes, but the peer may have issued
-    // copies that the leader has not come to expect: it has no barrier to wait
-    // on and lets a time pass that is thousands of times a copy's.
-    if (!ok && lane == 0) {
-      if (rank == 0) {
-        for (int j = i > S ? i - S : 0; j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1, &g_gemm_i8_timeout);
-      } else {
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 20000000ull) __nanosleep(1000);
       }
     }
   } else if (warp == 1) {
@@ -634,10 +622,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
-    if (lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
-    __syncwarp();
+  // Given up: the copies in flight land before shared memory goes away.  The
+  // leader's barriers count both CTAs' bytes, but the peer may have asked for
+  // stages that the leader has not come to: it has no barrier to wait on and
+  // lets a time pass that is thousands of times a copy's.
+  if (*abort && warp == 0 && lane == 0) {
+    if (rank == 0) {
+      for (int64_t j = issued > S ? issued - S : 0; j < issued; ++j)
+        mbar_drain(&full[j % S], uint32_t(j / S) & 1u, &g_gemm_i8_timeout);
+    } else {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 20000000ull) __nanosleep(1000);
+    }
   }
+  if (warp == 1 && lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
+  __syncwarp();
   cluster_sync();           // no arrival or copy of the pair is left in flight
   if (warp == 1) {
     tc_fence_after();
