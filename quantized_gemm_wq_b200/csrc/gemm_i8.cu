@@ -7,9 +7,10 @@
 // int32 sums are exact, so a split of K needs no order.
 //
 // split kernel (a batch of up to 128 tokens): bound by the read of the
-//   weights.  128 weight rows (gated: 64 of the gate and the same 64 of the up
-//   projection) are the MMA's M side, the tokens, padded to a multiple of 32,
-//   its N side: every weight byte is read once.  K is split over a cluster
+//   weights.  Up to 128 weight rows (gated: half of them the gate's, half the
+//   same ones of the up projection) are the MMA's M side, as many as give every
+//   SM its share, the tokens, padded to a multiple of 32, its N side: every
+//   weight byte is read once.  K is split over a cluster
 //   when the tiles alone leave SMs idle: rank r owns the tokens r, r + ks, ...;
 //   every rank writes its int32 sums of them into the owner's shared memory,
 //   and after one cluster barrier the owner adds what it holds.
@@ -179,6 +180,7 @@ __device__ __forceinline__ void store_four(void* y, int64_t i, const float (&v)[
 struct alignas(64) SplitArgs {
   CUtensorMap tx, t0, t1;
   Linear L;
+  int rows;      // weight rows of a tile, a multiple of 16; the MMA's rows behind them are idle
   int mt;        // M padded to a multiple of 32, at most kSplitTokens
   int stages;
   int vec;       // rows of y start where a store of four outputs may
@@ -204,8 +206,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   const int ks = gridDim.y, kr = blockIdx.y;
   const int kb_all = int((L.K + kBK - 1) / kBK);
   const int kb0 = int(int64_t(kb_all) * kr / ks), nkb = int(int64_t(kb_all) * (kr + 1) / ks) - kb0;
-  constexpr int kOut = GATED ? 64 : 128;          // outputs per token of a tile
-  const int64_t n0 = int64_t(blockIdx.x) * kOut;
+  const int out_n = GATED ? p.rows / 2 : p.rows;  // outputs per token of a tile
+  const int64_t n0 = int64_t(blockIdx.x) * out_n;
   const uint32_t cols = mt <= 32 ? 32 : mt <= 64 ? 64 : 128;
 
   pdl_start();
@@ -251,9 +253,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
       uint8_t* w = ring + at.s * stage;
       const int k = (kb0 + i) * kBK;
       if (elect_one()) {
-        mbar_expect_tx(&full[at.s], stage);
+        mbar_expect_tx(&full[at.s], uint32_t(p.rows + mt) * kBK);
         tma_load_2d(w, &p.t0, &full[at.s], k, int(n0));
-        if constexpr (GATED) tma_load_2d(w + kTile / 2, &p.t1, &full[at.s], k, int(n0));
+        if constexpr (GATED) tma_load_2d(w + out_n * kBK, &p.t1, &full[at.s], k, int(n0));
         tma_load_2d(w + kTile, &p.tx, &full[at.s], k, 0);
       }
       ++issued;
@@ -278,10 +280,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   __syncwarp();
   // the scales of this thread's four outputs and of the tile's tokens, while
   // the first operands are on their way
-  constexpr int kGroups = kOut / 4, kTokens = kSplitThreads / kGroups;
-  const int j = threadIdx.x % kGroups;
+  const int groups = out_n / 4, token0 = threadIdx.x / groups, tokens = kSplitThreads / groups;
+  const int j = threadIdx.x - token0 * groups;
   const int64_t n = n0 + 4 * j;
-  const int left = int(min(int64_t(4), L.N - n));       // outputs of this thread inside the row
+  const int left = token0 < tokens ? int(min(int64_t(4), L.N - n)) : 0;   // outputs of this thread inside the row
   float s0[4], s1[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   // A thread takes four neighbouring outputs of a token; token t of this rank
   // is row kr + ks t of the tile.
   if (!*abort && left > 0) {
-    for (int t = threadIdx.x / kGroups; kr + ks * t < L.M; t += kTokens) {
+    for (int t = token0; kr + ks * t < L.M; t += tokens) {
       int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < kSplitMax; ++r)
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
           const int4 v = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + 4 * j);
           a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
           if constexpr (GATED) {
-            const int4 u = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + 64 + 4 * j);
+            const int4 u = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + out_n + 4 * j);
             b[0] += u.x; b[1] += u.y; b[2] += u.z; b[3] += u.w;
           }
         }
@@ -717,20 +719,39 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   SplitArgs p;
   p.L = L;
   p.mt = int((L.M + 31) / 32 * 32);
-  constexpr int kOut = GATED ? 64 : 128;
-  if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, kOut) ||
-      (GATED && !make_map(&p.t1, L.w1, L.K, L.N, L.ldw, kOut)))
-    return cudaErrorInvalidValue;
   const int eb = type_bytes(L.type);
   p.vec = reinterpret_cast<uintptr_t>(L.y) % (4 * eb) == 0 && (L.ldy * eb) % (4 * eb) == 0;
   const uint32_t stage = kTile + uint32_t(p.mt) * kBK;
-  const int64_t tiles = (L.N + kOut - 1) / kOut, kb = (L.K + kBK - 1) / kBK;
-  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  // Split K while all clusters are on the SMs at once, one CTA an SM (64 tokens,
-  // 4096 x 4096, 32 tiles: 11.0 us unsplit, 9.0 / 8.4 / 9.1 over 2 / 4 / 8
-  // CTAs; 11008 x 4096, 86 tiles: 12.9 unsplit, 14.2 over 2).
+  const int64_t kb = (L.K + kBK - 1) / kBK;
+  auto tiles_of = [&](int rows) { return (L.N + (GATED ? rows / 2 : rows) - 1) / (GATED ? rows / 2 : rows); };
+  // Rows of a tile and split of K: the least that one SM has to read, in stages
+  // of one row: for each of its tiles the rows of weights and the tokens, over
+  // its share of K.  A split adds an exchange, as much as 250 of these for each
+  // doubling, and its clusters have to be on the SMs at once, one CTA an SM;
+  // smaller tiles have to read a good deal less to be worth it, and were not
+  // for clusters of 4 and 8.  (64 tokens, 4096 x 4096: 11.0 us unsplit, 9.0 /
+  // 8.3 over 2 / 4 CTAs; 11008 x 4096: 13.2 us in 86 tiles of 128 rows, 12.3 in
+  // 138 of 80; 16 tokens, 1024 x 8192 over 8 CTAs: 5.8 with 128 rows, 6.1 with 80.)
   int ks = 1;
-  while (ks < kSplitMax && kb >= 4 * ks && tiles <= clusters_at_once<GATED>(dev, 2 * ks)) ks *= 2;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= kSplitMax && (c == 1 || kb >= 2 * c); c *= 2)
+    for (int rows = 128; rows >= (c <= 2 ? 64 : 128); rows -= 16) {
+      const int64_t t = tiles_of(rows);
+      if (c > 1 && t > clusters_at_once<GATED>(dev, c)) break;
+      const int64_t load = (c > 1 ? 1 : (t + nsm - 1) / nsm) * (rows + p.mt) * ((kb + c - 1) / c) +
+                           250 * (c >= 8 ? 3 : c / 2);
+      if (load < (rows < 128 ? best - best / 8 : best)) {
+        best = load;
+        ks = c;
+        p.rows = rows;
+      }
+    }
+  const int64_t tiles = tiles_of(p.rows);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  const int out_n = GATED ? p.rows / 2 : p.rows;
+  if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, out_n) ||
+      (GATED && !make_map(&p.t1, L.w1, L.K, L.N, L.ldw, out_n)))
+    return cudaErrorInvalidValue;
   const uint32_t parked = ks > 1 ? uint32_t(p.mt) * 512 : 0;
   // two CTAs an SM where there are more than SMs, else one with a deeper ring
   const uint32_t budget = (tiles * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
