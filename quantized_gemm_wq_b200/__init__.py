@@ -265,39 +265,37 @@ _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}                        # wq_act
 
 
 # The three calls below are made once per layer and token, so what they do on
-# the host is kept short: device indexes instead of device objects, and the
-# current stream's address without a Stream object (3 us by itself).
+# the host is kept short: one test of everything a good call has, and only where
+# it fails the tests that say what is wrong; device indexes instead of device
+# objects; the current stream's address without a Stream object (3 us by itself).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+_empty_strided = torch.empty_strided
 _INT8, _FP32 = torch.int8, torch.float32
 
 
-def _rows(t: torch.Tensor, what: str):
-    """(rows, columns, row stride) of a 2-D CUDA tensor whose columns are adjacent."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
+def _need_matrix(t: torch.Tensor, what: str, dtypes=(_INT8,), dev=None) -> None:
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be of type " + " or ".join(str(d) for d in dtypes))
+    if t.dim() != 2 or not t.is_cuda or (dev is not None and t.get_device() != dev):
+        raise ValueError(f"{what} must be a 2-D CUDA tensor, all operands on one device")
+    if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{what} must have adjacent columns (stride 1)")
-    # the stride of a single row is never taken: any valid one will do
-    return rows, cols, ld if rows > 1 else (cols + 15) // 16 * 16
 
 
-def _codes(t: torch.Tensor, what: str):
-    if t.dtype is not _INT8:
-        raise ValueError(f"{what} must be int8 codes")
-    return _rows(t, what)
-
-
-def _scales(t: torch.Tensor, n: int, dev: int, what: str) -> int:
+def _need_scales(t: torch.Tensor, n: int, dev: int, what: str) -> None:
     if t.dtype is not _FP32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous fp32 [{n}] tensor on the codes' device")
-    return t.data_ptr()
 
 
-def _call(fn, where: str, dev: int, stream, *args) -> None:
-    """fn(*args, stream) with `dev` current: its current stream when `stream` is None."""
-    if dev == torch.cuda.current_device():
+def _pad16(n: int) -> int:
+    # for the stride of a single row, which is never taken: any valid one will do
+    return (n + 15) // 16 * 16
+
+
+def _run(fn, where: str, dev: int, stream, args) -> None:
+    """fn(*args, stream) with `dev` current, on its current stream when `stream` is None."""
+    if dev == _current_device():
         st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
@@ -309,25 +307,24 @@ def _call(fn, where: str, dev: int, stream, *args) -> None:
 def _empty(size, strides, dtype, x, stream):
     """Uninitialised memory on x's device, of the stream that will write it."""
     if stream is None:
-        return torch.empty_strided(size, strides, dtype=dtype, device=x.device)
+        return _empty_strided(size, strides, dtype=dtype, device=x.device)
     if stream.device != x.device:
         raise ValueError("stream must be one of the operands' device")
     with torch.cuda.stream(stream):
-        return torch.empty_strided(size, strides, dtype=dtype, device=x.device)
+        return _empty_strided(size, strides, dtype=dtype, device=x.device)
 
 
-def _output(y, M: int, N: int, dtype, x, stream, what: str):
+def _output(y, M: int, N: int, dtype, x, stream):
     """The output (made on x's device if None), its row stride and its wq_type."""
     if y is None:
         yt = _TYPES.get(dtype)
         if yt is None:
             raise ValueError("dtype must be torch.bfloat16, torch.float16 or torch.float32")
         return _empty((M, N), (N, 1), dtype, x, stream), N, yt
-    yt = _TYPES.get(y.dtype)
-    if yt is None or y.shape != (M, N) or y.get_device() != x.get_device():
-        raise ValueError(f"{what} must be a bf16, fp16 or fp32 [{M}, {N}] tensor on the codes' device")
-    ld = _rows(y, what)[2]
-    return y, ld if M > 1 else max(ld, N), yt
+    _need_matrix(y, "the output", tuple(_TYPES), x.get_device())
+    if y.shape != (M, N):
+        raise ValueError(f"the output must be [{M}, {N}]")
+    return y, y.stride(0) if M > 1 else N, _TYPES[y.dtype]
 
 
 def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
@@ -335,27 +332,30 @@ def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     -> (int8 codes [R, K], fp32 scales [R]), ``x ~ codes * scales[:, None]``.
     The codes' rows start at multiples of 16 bytes (128 for K > 1024), so for
     other K they do not lie side by side."""
-    xt = _TYPES.get(x.dtype)
-    if xt is None:
-        raise ValueError("x must be bf16, fp16 or fp32")
-    R, K, ldx = _rows(x, "x")
-    dev = x.get_device()
+    xt, dev = _TYPES.get(x.dtype), x.get_device()
+    if xt is None or dev < 0 or x.dim() != 2:
+        _need_matrix(x, "x", tuple(_TYPES))
+    R, K = x.shape
+    ldx, step = x.stride()
+    if step != 1:
+        _need_matrix(x, "x", tuple(_TYPES))
     if codes is None:
         # whole 128-byte lines a row where that costs little: the tensor-core
         # kernels fetch rows in pieces of 128 bytes (333 x 5003 -> 4992: 17.4 us
         # with rows of 5008 bytes, 13.7 with 5120)
-        ldc = (K + 127) // 128 * 128 if K > 1024 else (K + 15) // 16 * 16
+        ldc = (K + 127) // 128 * 128 if K > 1024 else _pad16(K)
         codes = _empty((R, K), (ldc, 1), _INT8, x, stream)
     else:
-        ldc = _codes(codes, "codes")[2]
-        if codes.shape != x.shape or codes.get_device() != dev:
-            raise ValueError("codes must have x's shape and device")
+        _need_matrix(codes, "codes", dev=dev)
+        if codes.shape != x.shape:
+            raise ValueError("codes must have x's shape")
+        ldc = codes.stride(0) if R > 1 else _pad16(K)
     if scales is None:
         scales = _empty((R,), (1,), _FP32, x, stream)
-        sp = scales.data_ptr()
     else:
-        sp = _scales(scales, R, dev, "scales")
-    _call(lib.wq_quantize_i8, "wq_quantize_i8", dev, stream, x.data_ptr(), xt, R, K, ldx, codes.data_ptr(), ldc, sp)
+        _need_scales(scales, R, dev, "scales")
+    _run(lib.wq_quantize_i8, "wq_quantize_i8", dev, stream,
+         (x.data_ptr(), xt, R, K, ldx if R > 1 else K, codes.data_ptr(), ldc, scales.data_ptr()))
     return codes, scales
 
 
@@ -364,15 +364,27 @@ def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     """``y[m, n] = x_scales[m] * w_scales[n] * sum_k x[m, k] w[n, k]`` for int8
     codes ``x`` [M, K] and ``w`` [N, K] -> ``y`` [M, N] of ``dtype`` (or the
     given ``y``'s type).  Row strides of codes are multiples of 16."""
-    M, K, ldx = _codes(x, "x")
-    N, Kw, ldw = _codes(w, "w")
     dev = x.get_device()
-    if Kw != K or w.get_device() != dev:
-        raise ValueError("w must be [N, K] with x's K, on x's device")
-    xs, ws = _scales(x_scales, M, dev, "x_scales"), _scales(w_scales, N, dev, "w_scales")
-    y, ldy, yt = _output(y, M, N, dtype, x, stream, "y")
-    _call(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w.data_ptr(), ldw, ws,
-          y.data_ptr(), yt, ldy)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be 2-D CUDA tensors")
+    M, K = x.shape
+    N, Kw = w.shape
+    ldx, xstep = x.stride()
+    ldw, wstep = w.stride()
+    if not (x.dtype is _INT8 and w.dtype is _INT8 and K == Kw and xstep == 1 and wstep == 1 and dev >= 0
+            and w.get_device() == dev and x_scales.dtype is _FP32 and w_scales.dtype is _FP32
+            and x_scales.shape == (M,) and w_scales.shape == (N,) and x_scales.get_device() == dev
+            and w_scales.get_device() == dev and x_scales.is_contiguous() and w_scales.is_contiguous()):
+        _need_matrix(x, "x")
+        _need_matrix(w, "w", dev=dev)
+        if Kw != K:
+            raise ValueError("w must be [N, K] with x's K")
+        _need_scales(x_scales, M, dev, "x_scales")
+        _need_scales(w_scales, N, dev, "w_scales")
+    y, ldy, yt = _output(y, M, N, dtype, x, stream)
+    _run(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream,
+         (x.data_ptr(), ldx if M > 1 else _pad16(K), x_scales.data_ptr(), M, N, K, w.data_ptr(),
+          ldw if N > 1 else _pad16(K), w_scales.data_ptr(), y.data_ptr(), yt, ldy))
     return y
 
 
@@ -385,14 +397,31 @@ def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, g
     at = _ACTS.get(act)
     if at is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    M, K, ldx = _codes(x, "x")
-    N, Kw, ldw = gate = _codes(w_gate, "w_gate")
     dev = x.get_device()
-    if Kw != K or _codes(w_up, "w_up") != gate or w_gate.get_device() != dev or w_up.get_device() != dev:
-        raise ValueError("w_gate and w_up must be [N, K] with x's K and one row stride, on x's device")
-    xs = _scales(x_scales, M, dev, "x_scales")
-    gs, us = _scales(gate_scales, N, dev, "gate_scales"), _scales(up_scales, N, dev, "up_scales")
-    h, ldh, ht = _output(h, M, N, dtype, x, stream, "h")
-    _call(lib.wq_gated_i8, "wq_gated_i8", dev, stream, x.data_ptr(), ldx, xs, M, N, K, w_gate.data_ptr(), gs,
-          w_up.data_ptr(), us, ldw, at, h.data_ptr(), ht, ldh)
+    if x.dim() != 2 or w_gate.dim() != 2 or w_up.dim() != 2:
+        raise ValueError("x, w_gate and w_up must be 2-D CUDA tensors")
+    M, K = x.shape
+    N, Kw = w_gate.shape
+    ldx, xstep = x.stride()
+    strides = ldw, wstep = w_gate.stride()
+    if not (x.dtype is _INT8 and w_gate.dtype is _INT8 and w_up.dtype is _INT8 and K == Kw and xstep == 1
+            and wstep == 1 and w_up.shape == w_gate.shape and w_up.stride() == strides and dev >= 0
+            and w_gate.get_device() == dev and w_up.get_device() == dev and x_scales.dtype is _FP32
+            and gate_scales.dtype is _FP32 and up_scales.dtype is _FP32 and x_scales.shape == (M,)
+            and gate_scales.shape == (N,) and up_scales.shape == (N,) and x_scales.get_device() == dev
+            and gate_scales.get_device() == dev and up_scales.get_device() == dev and x_scales.is_contiguous()
+            and gate_scales.is_contiguous() and up_scales.is_contiguous()):
+        _need_matrix(x, "x")
+        _need_matrix(w_gate, "w_gate", dev=dev)
+        _need_matrix(w_up, "w_up", dev=dev)
+        if Kw != K or w_up.shape != w_gate.shape or (N > 1 and w_up.stride(0) != ldw):
+            raise ValueError("w_gate and w_up must be [N, K] with x's K and one row stride")
+        _need_scales(x_scales, M, dev, "x_scales")
+        _need_scales(gate_scales, N, dev, "gate_scales")
+        _need_scales(up_scales, N, dev, "up_scales")
+    h, ldh, ht = _output(h, M, N, dtype, x, stream)
+    _run(lib.wq_gated_i8, "wq_gated_i8", dev, stream,
+         (x.data_ptr(), ldx if M > 1 else _pad16(K), x_scales.data_ptr(), M, N, K, w_gate.data_ptr(),
+          gate_scales.data_ptr(), w_up.data_ptr(), up_scales.data_ptr(), ldw if N > 1 else _pad16(K), at,
+          h.data_ptr(), ht, ldh))
     return h
