@@ -261,7 +261,9 @@ wq_status wq_gemm_grouped_noalloc(const wq_linear* linears, int count, int64_t M
  *     of 16; other pointers need the alignment of their element type only;
  *   - 1 <= K <= 131071 (a sum of K products of 8-bit codes fits int32); any K,
  *     no multiple is needed;
- *   - outputs must not overlap inputs.
+ *   - outputs must not overlap inputs;
+ *   - no workspace is needed, and calls may be captured into graphs; on
+ *     different streams they are independent of each other.
  */
 typedef enum { WQ_TYPE_BF16 = 0, WQ_TYPE_F16 = 1, WQ_TYPE_F32 = 2 } wq_type;
 typedef enum {
@@ -297,7 +299,9 @@ wq_status wq_quantize_i8(const void* x, wq_type x_type, int64_t R, int64_t K, in
  * The sum is exact (int32); it is converted to fp32, multiplied by x_scales[m],
  * then by w_scales[n] (three fp32 roundings) and rounded once to y_type.  So y
  * does not depend on M, on the other rows or on which kernel ran, bit for bit.
- * A non-finite scale gives a non-finite row or column.
+ * A NaN scale gives a row or column of NaNs, an infinite one infinities (NaN
+ * where the sum is 0).  M <= 8 runs on warp-level MMAs, 9..128 and more on
+ * two tensor-core kernels.
  */
 wq_status wq_gemm_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_t M, int64_t N, int64_t K,
                      const int8_t* w, int64_t ldw, const float* w_scales, void* y, wq_type y_type, int64_t ldy,

