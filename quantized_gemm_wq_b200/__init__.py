@@ -295,6 +295,8 @@ def _pad16(n: int) -> int:
 
 def _run(fn, where: str, dev: int, stream, args) -> None:
     """fn(*args, stream) with `dev` current, on its current stream when `stream` is None."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("stream must be one of the operands' device")
     if dev == _current_device():
         st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
@@ -308,8 +310,6 @@ def _empty(size, strides, dtype, x, stream):
     """Uninitialised memory on x's device, of the stream that will write it."""
     if stream is None:
         return _empty_strided(size, strides, dtype=dtype, device=x.device)
-    if stream.device != x.device:
-        raise ValueError("stream must be one of the operands' device")
     with torch.cuda.stream(stream):
         return _empty_strided(size, strides, dtype=dtype, device=x.device)
 

@@ -33,12 +33,22 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Weights are read once: past L1.
+// Weights are read once: past L1.  Not as read-only data (.nc): this kernel may
+// start before the one ahead, which may write what is read here, has ended.
 __device__ __forceinline__ uint4 ld_stream(const int8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_tokens(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -87,7 +97,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L)
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int h = 0; h < 2; ++h) c[u].a[i][r][h] = ld_stream(wp[r][h] + k);
-        c[u].x[i] = xlive ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : make_uint4(0, 0, 0, 0);
+        c[u].x[i] = xlive ? ld_tokens(xp + k) : make_uint4(0, 0, 0, 0);
       }
   };
   auto feed = [&](const uint4 (&a)[RT][2], const uint4& x) {
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L)
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int h = 0; h < 2; ++h) a[r][h] = valid >= 16 ? ld_stream(wp[r][h] + k) : ld_part(wp[r][h] + k, valid);
-      if (xlive) x = valid >= 16 ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : ld_part(xp + k, valid);
+      if (xlive) x = valid >= 16 ? ld_tokens(xp + k) : ld_part(xp + k, valid);
       feed(a, x);
     }
 

@@ -66,7 +66,8 @@ __device__ __forceinline__ void store_one(void* y, int64_t i, float v, int type)
 
 // Programmatic dependent launch: the next kernel of the stream may set itself
 // up from here on; this one touches no memory of its own before the kernels
-// ahead of it are complete.
+// ahead of it are complete.  (So nothing is loaded as read-only data, .nc or
+// __ldg, in these kernels: what they read may be written after they start.)
 __device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -86,14 +86,14 @@ struct Vec {
 // VE elements from k on, all inside the row.
 template <int TYPE, bool ALIGNED>
 __device__ __forceinline__ uint4 load_vec(const typename Vec<TYPE>::Elem* p) {
-  if constexpr (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(p));
+  if constexpr (ALIGNED) return *reinterpret_cast<const uint4*>(p);
   uint32_t w[4];
   if constexpr (TYPE == kF32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __ldg(p + i);
+    for (int i = 0; i < 4; ++i) w[i] = p[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = uint32_t(__ldg(p + 2 * i)) | uint32_t(__ldg(p + 2 * i + 1)) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = uint32_t(p[2 * i]) | uint32_t(p[2 * i + 1]) << 16;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -104,8 +104,8 @@ __device__ __forceinline__ uint4 load_tail(const typename Vec<TYPE>::Elem* p, in
 #pragma unroll
   for (int i = 0; i < Vec<TYPE>::VE; ++i)
     if (i < n) {
-      if constexpr (TYPE == kF32) w[i] = __ldg(p + i);
-      else w[i >> 1] |= uint32_t(__ldg(p + i)) << (16 * (i & 1));
+      if constexpr (TYPE == kF32) w[i] = p[i];
+      else w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -178,7 +178,7 @@ __device__ __forceinline__ float inverse(float a, float s) {
 // 2^lw warps per row, several rows per CTA of THREADS threads.  NV > 0: each thread
 // holds its NV vectors of the row in registers; NV = 0: two passes over memory.
 template <int TYPE, int NV, bool ALIGNED, int THREADS>
-__global__ void __launch_bounds__(THREADS) quantize_i8_kernel(const void* __restrict__ xv, int64_t R, int64_t K,
+__global__ void __launch_bounds__(THREADS) quantize_i8_kernel(const void* xv, int64_t R, int64_t K,
                                                                int64_t ldx, int8_t* __restrict__ codes, int64_t ldc,
                                                                float* __restrict__ scales, int lw) {
   using V = Vec<TYPE>;

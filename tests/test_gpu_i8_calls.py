@@ -184,6 +184,71 @@ def test_results_past_2_to_32_elements():
     assert (qs[:33990] == 0).all() and not q[:33990:997].any()
 
 
+def _first_call_child(q, M):
+    import sys
+    sys.path.insert(0, ROOT)
+    try:
+        import torch
+
+        import quantized_gemm_wq_b200 as wq
+        K, N = 512, 768
+        x = torch.randn(M, K, device="cuda").bfloat16()
+        w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+        ws = torch.rand(N, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):                     # the process's first calls are the captured ones
+            c, s = wq.wq_quantize_i8(x)
+            y = wq.wq_gemm_i8(c, s, w, ws)
+            h = wq.wq_gated_i8(c, s, w, ws, w, ws)
+        g.replay()
+        torch.cuda.synchronize()
+        c2, s2 = wq.wq_quantize_i8(x)
+        q.put(bool(torch.equal(c, c2) and torch.equal(y, wq.wq_gemm_i8(c2, s2, w, ws))
+                   and torch.equal(h, wq.wq_gated_i8(c2, s2, w, ws, w, ws))))
+    except Exception as e:  # noqa: BLE001
+        q.put(repr(e))
+
+
+@pytest.mark.parametrize("M", [4, 40, 300])
+def test_first_calls_may_be_captured(M):
+    ctx = mp.get_context("spawn")
+    q = ctx.Queue()
+    pr = ctx.Process(target=_first_call_child, args=(q, M))
+    pr.start()
+    res = q.get(timeout=300)
+    pr.join(60)
+    assert res is True, res
+
+
+@pytest.mark.parametrize("M", [1, 8, 100, 300])
+def test_tokens_rewritten_just_before_the_product(M):
+    """The same codes and scales buffers for other tokens at every step, with the products of
+    the steps before still reading them: no step sees what an earlier one left in a cache."""
+    m = wq()
+    rng = np.random.default_rng([7, M])
+    N, K = 2304, 512
+    w, wh = codes(rng, N, K)
+    ws, wsh = scales(rng, N)
+    xs = [torch.from_numpy(rng.standard_normal((M, K))).bfloat16().cuda() for _ in range(5)]
+    want = []
+    for x in xs:
+        q, qs = quantize_ref(x.double().cpu().numpy())
+        want.append(torch.from_numpy(scaled_f32(product(q, wh), qs, wsh)).bfloat16().cuda())
+    buf, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    ys = torch.empty(300, M, N, dtype=torch.bfloat16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):                         # back to back on the GPU
+        for i in range(300):
+            m.wq_quantize_i8(xs[i % 5], codes=buf, scales=s)
+            m.wq_gemm_i8(buf, s, w, ws, y=ys[i])
+    for _ in range(3):
+        ys.zero_()
+        g.replay()
+        for i in range(300):
+            assert torch.equal(ys[i], want[i % 5]), i
+
+
 def _child(q):
     import sys
     sys.path.insert(0, ROOT)
