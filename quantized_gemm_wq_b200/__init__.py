@@ -330,8 +330,8 @@ def _output(y, M: int, N: int, dtype, x, stream):
 def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     """Quantise every row of bf16/fp16/fp32 ``x`` [R, K] (CUDA, any row stride)
     -> (int8 codes [R, K], fp32 scales [R]), ``x ~ codes * scales[:, None]``.
-    The codes' rows start at multiples of 16 bytes (128 for K > 1024), so for
-    other K they do not lie side by side."""
+    The codes' rows start at multiples of 32 bytes, so for other K they do not
+    lie side by side."""
     xt, dev = _TYPES.get(x.dtype), x.get_device()
     if xt is None or dev < 0 or x.dim() != 2:
         _need_matrix(x, "x", tuple(_TYPES))
@@ -340,10 +340,9 @@ def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     if step != 1:
         _need_matrix(x, "x", tuple(_TYPES))
     if codes is None:
-        # whole 128-byte lines a row where that costs little: the tensor-core
-        # kernels fetch rows in pieces of 128 bytes (333 x 5003 -> 4992: 17.4 us
-        # with rows of 5008 bytes, 13.7 with 5120)
-        ldc = (K + 127) // 128 * 128 if K > 1024 else _pad16(K)
+        # rows on 32 bytes, L2's sectors: the tensor-core kernels take a quarter
+        # longer where they are on 16 (2048 x 5120 -> 5120: 48 against 38 us)
+        ldc = (K + 31) // 32 * 32
         codes = _empty((R, K), (ldc, 1), _INT8, x, stream)
     else:
         _need_matrix(codes, "codes", dev=dev)

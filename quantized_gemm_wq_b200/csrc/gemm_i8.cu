@@ -6,8 +6,8 @@
 // MMAs of K = 32 each.  Bytes past K and rows past the matrices read as zero.
 // int32 sums are exact, so a split of K needs no order.
 //
-// split kernel (a batch of up to 128 tokens): bound by the read of the
-//   weights.  Up to 128 weight rows (gated: half of them the gate's, half the
+// split kernel (up to 128 tokens, and more where there are few outputs): bound
+//   by the read of the weights.  Up to 128 weight rows (gated: half of them the gate's, half the
 //   same ones of the up projection) are the MMA's M side, as many as give every
 //   SM its share, the tokens, padded to a multiple of 32, its N side: every
 //   weight byte is read once.  K is split over a cluster
@@ -186,7 +186,7 @@ struct alignas(64) SplitArgs {
   CUtensorMap tx, t0, t1;
   Linear L;
   int rows;      // weight rows of a tile, a multiple of 16; the MMA's rows behind them are idle
-  int mt;        // M padded to a multiple of 32, at most kSplitTokens
+  int mt;        // tokens of a tile: a multiple of 32, at most kSplitTokens
   int stages;
   int vec;       // rows of y start where a store of four outputs may
 };
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   const int kb_all = int((L.K + kBK - 1) / kBK);
   const int kb0 = int(int64_t(kb_all) * kr / ks), nkb = int(int64_t(kb_all) * (kr + 1) / ks) - kb0;
   const int out_n = GATED ? p.rows / 2 : p.rows;  // outputs per token of a tile
-  const int64_t n0 = int64_t(blockIdx.x) * out_n;
+  const int64_t n0 = int64_t(blockIdx.x) * out_n, m0 = int64_t(blockIdx.z) * mt;
   const uint32_t cols = mt <= 32 ? 32 : mt <= 64 ? 64 : 128;
 
   pdl_start();
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
         mbar_expect_tx(&full[at.s], uint32_t(p.rows + mt) * kBK);
         tma_load_2d(w, &p.t0, &full[at.s], k, int(n0));
         if constexpr (GATED) tma_load_2d(w + out_n * kBK, &p.t1, &full[at.s], k, int(n0));
-        tma_load_2d(w + kTile, &p.tx, &full[at.s], k, 0);
+        tma_load_2d(w + kTile, &p.tx, &full[at.s], k, int(m0));
       }
       ++issued;
     }
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     s0[i] = i < left ? L.s0[n + i] : 0.0f;
     s1[i] = GATED && i < left ? L.s1[n + i] : 0.0f;
   }
-  if (threadIdx.x < L.M) xscale[threadIdx.x] = L.xs[threadIdx.x];
+  const int mend = int(min(int64_t(mt), L.M - m0));     // tokens of this tile
+  if (threadIdx.x < mend) xscale[threadIdx.x] = L.xs[m0 + threadIdx.x];
   bool ok = wait_for(&done, 0, abort);
   ok = __all_sync(0xffffffffu, ok);   // tcgen05.ld needs the whole warp
 
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   // A thread takes four neighbouring outputs of a token; token t of this rank
   // is row kr + ks t of the tile.
   if (!*abort && left > 0) {
-    for (int t = token0; kr + ks * t < L.M; t += tokens) {
+    for (int t = token0; kr + ks * t < mend; t += tokens) {
       int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < kSplitMax; ++r)
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
         v[e] = scaled(a[e], sx, s0[e]);
         if constexpr (GATED) v[e] = apply_act(v[e], L.act) * scaled(b[e], sx, s1[e]);
       }
-      store_four(L.y, m * L.ldy + n, v, left, L.type, p.vec);
+      store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
     }
   }
   tc_fence_before();
@@ -685,6 +686,12 @@ cudaError_t current_device(int* dev) {
   return *dev >= 0 && *dev < 64 ? cudaSuccess : cudaErrorInvalidDevice;
 }
 
+template <bool GATED>
+cudaError_t allow_split(int dev) {
+  static std::atomic<bool> set[64];
+  return allow_smem(gemm_i8_split_kernel<GATED>, kSmemMax - 4096, set, dev);
+}
+
 // How many clusters of ks CTAs of the split kernel, one CTA an SM, run at once:
 // fewer than the SMs divided by ks, as a cluster stays within one group of SMs
 // (16 clusters of 8 took two rounds: 14.0 us against 9.1 over 4).
@@ -704,13 +711,53 @@ int clusters_at_once(int dev, int ks) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_i8_split_kernel<GATED>, &cfg) != cudaSuccess || n < 1) {
+    if (allow_split<GATED>(dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gemm_i8_split_kernel<GATED>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
-      n = 1;
+      return 1;
     }
     cached[dev][ks].store(n, std::memory_order_relaxed);
   }
   return n;
+}
+
+struct SplitPlan {
+  int mt, rows, ks;
+  int64_t tiles_n, tiles_m;
+  int64_t load;      // what one SM has to read, in stages of one row (about 0.6 ns each)
+};
+
+// Rows of a tile and split of K: the least that one SM has to read: for each of
+// its tiles the rows of weights and the tokens, over its share of K.  A split
+// adds an exchange, as much as 250 of these for each doubling, and its clusters
+// have to be on the SMs at once, one CTA an SM; smaller tiles have to read a
+// good deal less to be worth it, and were not for clusters of 4 and 8.  (64
+// tokens, 4096 x 4096: 11.0 us unsplit, 9.0 / 8.3 over 2 / 4 CTAs; 11008 x 4096:
+// 13.2 us in 86 tiles of 128 rows, 12.3 in 138 of 80; 16 tokens, 1024 x 8192
+// over 8 CTAs: 5.8 with 128 rows, 6.1 with 80.)
+template <bool GATED>
+SplitPlan split_plan(const Linear& L, int dev) {
+  SplitPlan p = {};
+  const int nsm = sm_count(dev);
+  const int64_t kb = (L.K + kBK - 1) / kBK;
+  p.mt = L.M > kSplitTokens ? kSplitTokens : int((L.M + 31) / 32 * 32);
+  p.tiles_m = (L.M + p.mt - 1) / p.mt;
+  p.load = INT64_MAX;
+  for (int c = 1; c <= kSplitMax && (c == 1 || kb >= 2 * c); c *= 2)
+    for (int rows = 128; rows >= (c <= 2 ? 64 : 128); rows -= 16) {
+      const int out_n = GATED ? rows / 2 : rows;
+      const int64_t tn = (L.N + out_n - 1) / out_n, t = tn * p.tiles_m;
+      if (c > 1 && t > clusters_at_once<GATED>(dev, c)) break;
+      const int64_t load = (c > 1 ? 1 : (t + nsm - 1) / nsm) * (rows + p.mt) * ((kb + c - 1) / c) +
+                           250 * (c >= 8 ? 3 : c / 2);
+      if (load < (rows < 128 ? p.load - p.load / 8 : p.load)) {
+        p.load = load;
+        p.ks = c;
+        p.rows = rows;
+        p.tiles_n = tn;
+      }
+    }
+  return p;
 }
 
 template <bool GATED>
@@ -718,52 +765,29 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   int dev;
   cudaError_t e = current_device(&dev);
   if (e != cudaSuccess) return e;
-  static std::atomic<bool> set[64];
-  if ((e = allow_smem(gemm_i8_split_kernel<GATED>, kSmemMax - 4096, set, dev)) != cudaSuccess) return e;
+  if ((e = allow_split<GATED>(dev)) != cudaSuccess) return e;
   const int nsm = sm_count(dev);
+  const SplitPlan plan = split_plan<GATED>(L, dev);
+  const int ks = plan.ks;
+  if (plan.tiles_n > 0x7fffffff || plan.tiles_m > 65535) return cudaErrorInvalidValue;
   SplitArgs p;
   p.L = L;
-  p.mt = int((L.M + 31) / 32 * 32);
+  p.mt = plan.mt;
+  p.rows = plan.rows;
   const int eb = type_bytes(L.type);
   p.vec = reinterpret_cast<uintptr_t>(L.y) % (4 * eb) == 0 && (L.ldy * eb) % (4 * eb) == 0;
   const uint32_t stage = kTile + uint32_t(p.mt) * kBK;
-  const int64_t kb = (L.K + kBK - 1) / kBK;
-  auto tiles_of = [&](int rows) { return (L.N + (GATED ? rows / 2 : rows) - 1) / (GATED ? rows / 2 : rows); };
-  // Rows of a tile and split of K: the least that one SM has to read, in stages
-  // of one row: for each of its tiles the rows of weights and the tokens, over
-  // its share of K.  A split adds an exchange, as much as 250 of these for each
-  // doubling, and its clusters have to be on the SMs at once, one CTA an SM;
-  // smaller tiles have to read a good deal less to be worth it, and were not
-  // for clusters of 4 and 8.  (64 tokens, 4096 x 4096: 11.0 us unsplit, 9.0 /
-  // 8.3 over 2 / 4 CTAs; 11008 x 4096: 13.2 us in 86 tiles of 128 rows, 12.3 in
-  // 138 of 80; 16 tokens, 1024 x 8192 over 8 CTAs: 5.8 with 128 rows, 6.1 with 80.)
-  int ks = 1;
-  int64_t best = INT64_MAX;
-  for (int c = 1; c <= kSplitMax && (c == 1 || kb >= 2 * c); c *= 2)
-    for (int rows = 128; rows >= (c <= 2 ? 64 : 128); rows -= 16) {
-      const int64_t t = tiles_of(rows);
-      if (c > 1 && t > clusters_at_once<GATED>(dev, c)) break;
-      const int64_t load = (c > 1 ? 1 : (t + nsm - 1) / nsm) * (rows + p.mt) * ((kb + c - 1) / c) +
-                           250 * (c >= 8 ? 3 : c / 2);
-      if (load < (rows < 128 ? best - best / 8 : best)) {
-        best = load;
-        ks = c;
-        p.rows = rows;
-      }
-    }
-  const int64_t tiles = tiles_of(p.rows);
-  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
   const int out_n = GATED ? p.rows / 2 : p.rows;
   if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, out_n) ||
       (GATED && !make_map(&p.t1, L.w1, L.K, L.N, L.ldw, out_n)))
     return cudaErrorInvalidValue;
   const uint32_t parked = ks > 1 ? uint32_t(p.mt) * 512 : 0;
   // two CTAs an SM where there are more than SMs, else one with a deeper ring
-  const uint32_t budget = (tiles * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
+  const uint32_t budget = (plan.tiles_n * plan.tiles_m * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
   p.stages = int((budget - 1024 - parked) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles), unsigned(ks));
+  cfg.gridDim = dim3(unsigned(plan.tiles_n), unsigned(ks), unsigned(plan.tiles_m));
   cfg.blockDim = dim3(kSplitThreads, 1, 1);
   cfg.dynamicSmemBytes = p.stages * stage + parked + 1024;
   cfg.stream = st;
@@ -779,6 +803,42 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<GATED>, p);
 }
 
+// Columns of a pair's tile: the fewest that one pair works through, counting a
+// tile's own cost as 32 of them.
+template <bool GATED>
+int pair_columns(const Linear& L, int pairs) {
+  const int64_t tm = (L.M + 255) / 256;
+  int64_t best = INT64_MAX;
+  int columns = 256;
+  for (int bn = 256; bn >= 64; bn -= GATED ? 64 : 32) {
+    const int out_n = GATED ? bn / 2 : bn;
+    const int64_t t = (tm * ((L.N + out_n - 1) / out_n) + pairs - 1) / pairs * (bn + 32);
+    if (t < best) {
+      best = t;
+      columns = bn;
+    }
+  }
+  return columns;
+}
+
+// More than 128 tokens: the pair kernel, but for few outputs and long sums, which
+// leave most pairs without a tile.  Both costs in the split plan's units: a
+// pair's stage takes its read or its MMAs (1.75 a column), its tile 2800 (gated
+// 4300) more than a split tile, which has an epilogue of its own of 14 a token.
+// The split kernel has to be well ahead: measured, split / pair, 256 tokens,
+// 1024 x 8192 11.0 / 13.5 us, gated 1024 x 4096 9.1 / 11.7; 160 tokens, 256 x
+// 4096 6.3 / 8.5; but 512 tokens, 1024 x 4096 9.1 / 8.9, 160, 4096 x 4096 12.3 / 9.8.
+template <bool GATED>
+bool prefer_split(const Linear& L, int dev) {
+  const int pairs = sm_count(dev) / 2, bn = pair_columns<GATED>(L, pairs), out_n = GATED ? bn / 2 : bn;
+  const int64_t kb = (L.K + kBK - 1) / kBK;
+  const int64_t rounds = ((L.M + 255) / 256 * ((L.N + out_n - 1) / out_n) + pairs - 1) / pairs;
+  const int64_t stage = 128 + bn / 2 > bn * 7 / 4 ? 128 + bn / 2 : bn * 7 / 4;
+  if (rounds > 1) return false;
+  const SplitPlan s = split_plan<GATED>(L, dev);
+  return 2 * (s.load + 14 * s.mt) < kb * stage + (GATED ? 4300 : 2800);
+}
+
 template <bool GATED>
 cudaError_t pair(const Linear& L, cudaStream_t st) {
   int dev;
@@ -790,16 +850,7 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
   PairArgs p;
   p.L = L;
   const int64_t tm = (L.M + 255) / 256;
-  double best = 1e300;
-  p.bn = 256;
-  for (int bn = 256; bn >= 64; bn -= GATED ? 64 : 32) {
-    const int64_t tiles = tm * ((L.N + (GATED ? bn / 2 : bn) - 1) / (GATED ? bn / 2 : bn));
-    const double t = double((tiles + pairs - 1) / pairs) * (bn + 32);
-    if (t < best - 1e-9) {
-      best = t;
-      p.bn = bn;
-    }
-  }
+  p.bn = pair_columns<GATED>(L, pairs);
   const int out_n = GATED ? p.bn / 2 : p.bn;
   const int64_t tn = (L.N + out_n - 1) / out_n;
   if (tm * tn > 0x7fffffff) return cudaErrorInvalidValue;
@@ -829,17 +880,18 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_split(const Linear& L, cudaStream_t st) {
-  return L.act == kNone ? split<false>(L, st) : split<true>(L, st);
-}
-cudaError_t launch_pair(const Linear& L, cudaStream_t st) {
-  return L.act == kNone ? pair<false>(L, st) : pair<true>(L, st);
-}
-
 cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
-  if (L.M <= 8) return launch_gemv(L, st);
-  if (L.M <= kSplitTokens) return launch_split(L, st);
-  return launch_pair(L, st);
+  const bool gated = L.act != kNone;
+  if (L.M <= kGemvTokens) return launch_gemv(L, st);
+  bool few = L.M <= kSplitTokens;
+  if (!few) {
+    int dev;
+    const cudaError_t e = current_device(&dev);
+    if (e != cudaSuccess) return e;
+    few = gated ? prefer_split<true>(L, dev) : prefer_split<false>(L, dev);
+  }
+  if (few) return gated ? split<true>(L, st) : split<false>(L, st);
+  return gated ? pair<true>(L, st) : pair<false>(L, st);
 }
 
 bool gemm_read_and_clear_timeout(cudaError_t* err) {

@@ -23,7 +23,7 @@ namespace i8 {
 namespace {
 
 constexpr int kMaxWarps = 16;
-constexpr int kTokens = 8;
+constexpr int kTokens = kGemvTokens;    // the MMA's columns
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {

@@ -73,9 +73,9 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 cudaError_t launch_quantize(const void* x, int type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
                             int64_t ldc, float* scales, cudaStream_t st);
+// Up to kGemvTokens tokens.
+constexpr int kGemvTokens = 8;
 cudaError_t launch_gemv(const Linear& L, cudaStream_t st);
-cudaError_t launch_split(const Linear& L, cudaStream_t st);
-cudaError_t launch_pair(const Linear& L, cudaStream_t st);
 bool gemm_read_and_clear_timeout(cudaError_t* err);
 
 // The kernel of one call (arguments already checked by the C ABI).
