@@ -106,8 +106,10 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
       "l"(map), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
+// Relaxed: it tells of tensor-memory reads, which have ended before it, and of
+// no memory; a release would wait for the warp's stores of the tile.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -154,6 +156,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 16 columns; wait16 is where their values begin to exist.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -196,8 +214,9 @@ constexpr int kSplitTokens = 128;
 constexpr int kSplitMax = 8;            // CTAs of a cluster along K
 constexpr int kMaxStages = 10;
 
-template <bool GATED>
+template <int ACT>
 __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const __grid_constant__ SplitArgs p) {
+  constexpr bool GATED = ACT != kNone;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e] = scaled(a[e], sx, s0[e]);
-        if constexpr (GATED) v[e] = apply_act(v[e], L.act) * scaled(b[e], sx, s1[e]);
+        if constexpr (GATED) v[e] = apply_act(v[e], ACT) * scaled(b[e], sx, s1[e]);
       }
       store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
     }
@@ -436,9 +455,10 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm
   tn = r / rows;
 }
 
-template <bool GATED>
+template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_i8_pair_kernel(const __grid_constant__ PairArgs p) {
+  constexpr bool GATED = ACT != kNone;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kPairStages];      // leader's: both CTAs' copies landed
@@ -549,79 +569,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     // Warp w reads tensor-memory lanes 32 (w % 4) .. (rows of this CTA's 128
-    // tokens), and of the 32-column blocks of outputs every other one.
+    // tokens), and of the 32-column blocks of outputs every other one, in two
+    // halves: while one is worked on the next is on its way to registers.
     const int q = warp & 3, half = (warp - 2) >> 2;
     float* wscale = wscale_all[warp - 2];
     uint8_t* out = out_all[warp - 2];
+    const int eb = L.type == kF32 ? 4 : 2;
     bool ok = true;
     int n = 0;
+    // this lane's scales of a tile: of columns lane, lane + 32, ... (gated: the
+    // gate's, then the up projection's) and of its token
+    float ws[8], sx;
+    auto load_scales = [&](int t) {
+      int tm, tn;
+      tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int64_t m = int64_t(tm) * 256 + rank * 128 + 32 * q + lane, n0 = int64_t(tn) * out_n;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = lane + 32 * i;
+        const bool up = GATED && c >= out_n;
+        const int64_t nn = n0 + (up ? c - out_n : c);
+        ws[i] = c < bn && nn < L.N ? (up ? L.s1[nn] : L.s0[nn]) : 0.0f;
+      }
+      sx = m < L.M ? L.xs[m] : 0.0f;
+    };
+    load_scales(blockIdx.x / 2);
     for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
       int tm, tn;
       tile_at(t, p.tiles_m, p.tiles_n, tm, tn);
       const int a = n & 1;
-      const int64_t m = int64_t(tm) * 256 + rank * 128 + 32 * q + lane;
+      const int64_t m = int64_t(tm) * 256 + rank * 128 + 32 * q;      // the warp's first token
       const int64_t n0 = int64_t(tn) * out_n;
-      // the columns' scales (gated: the gate's, then the up projection's); each
-      // warp keeps its own, as no warp may wait for one that has given up
+      // each warp keeps the columns' scales for itself, as no warp may wait for
+      // one that has given up; the next tile's are fetched meanwhile
       __syncwarp();
-      for (int c = lane; c < bn; c += 32) {
-        const int64_t nn = n0 + (GATED && c >= out_n ? c - out_n : c);
-        wscale[c] = nn < L.N ? (GATED && c >= out_n ? L.s1[nn] : L.s0[nn]) : 0.0f;
-      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wscale[lane + 32 * i] = ws[i];
       __syncwarp();
-      const float sx = m < L.M ? L.xs[m] : 0.0f;
+      const float s = sx;
+      if (t + step < tiles) load_scales(t + step);
       ok = wait_for(&acc_full[a], (n >> 1) & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + (uint32_t(32 * q) << 16) + uint32_t(a) * 256;
-      for (int c = 32 * half;; c += 64) {
-        uint32_t r[32], u[32];
-        if (c < out_n) {
-          tmem_ld32(base + uint32_t(c), r);
-          if constexpr (GATED) tmem_ld32(base + uint32_t(out_n + c), u);
-          tmem_wait_ld();
-        }
-        if (c + 64 >= out_n) {              // this warp's columns are read: the MMAs may have the accumulator
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(mapa(smem_u32(&acc_empty[a]), 0));
-        }
-        if (c < out_n) {
+      // 16 columns from c on, of this lane's token, into the staging row
+      auto work = [&](const uint32_t (&r)[16], const uint32_t (&u)[16], int c) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            float v[8];
+        for (int j = 0; j < 16; j += 8) {
+          float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-              const float4 s0 = *reinterpret_cast<const float4*>(wscale + c + j + i);
-              v[i] = scaled(int(r[j + i]), sx, s0.x);
-              v[i + 1] = scaled(int(r[j + i + 1]), sx, s0.y);
-              v[i + 2] = scaled(int(r[j + i + 2]), sx, s0.z);
-              v[i + 3] = scaled(int(r[j + i + 3]), sx, s0.w);
-              if constexpr (GATED) {
-                const float4 s1 = *reinterpret_cast<const float4*>(wscale + out_n + c + j + i);
-                v[i] = apply_act(v[i], L.act) * scaled(int(u[j + i]), sx, s1.x);
-                v[i + 1] = apply_act(v[i + 1], L.act) * scaled(int(u[j + i + 1]), sx, s1.y);
-                v[i + 2] = apply_act(v[i + 2], L.act) * scaled(int(u[j + i + 2]), sx, s1.z);
-                v[i + 3] = apply_act(v[i + 3], L.act) * scaled(int(u[j + i + 3]), sx, s1.w);
-              }
-            }
-            if (L.type == kF32) {
-              uint4* o = reinterpret_cast<uint4*>(out + lane * kOutRow + (j & 8) * 4);
-              o[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-              o[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-              if (j & 8) flush_rows(out, L, m - lane, n0 + c + j - 8, lane, p.vec);
-            } else {
-              *reinterpret_cast<uint4*>(out + lane * kOutRow + j * 2) =
-                  L.type == kBF16 ? make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                               pack_bf16(v[6], v[7]))
-                                  : make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]),
-                                               pack_f16(v[6], v[7]));
+          for (int i = 0; i < 8; i += 4) {
+            const float4 s0 = *reinterpret_cast<const float4*>(wscale + c + j + i);
+            v[i] = scaled(int(r[j + i]), s, s0.x);
+            v[i + 1] = scaled(int(r[j + i + 1]), s, s0.y);
+            v[i + 2] = scaled(int(r[j + i + 2]), s, s0.z);
+            v[i + 3] = scaled(int(r[j + i + 3]), s, s0.w);
+            if constexpr (GATED) {
+              const float4 s1 = *reinterpret_cast<const float4*>(wscale + out_n + c + j + i);
+              v[i] = apply_act(v[i], ACT) * scaled(int(u[j + i]), s, s1.x);
+              v[i + 1] = apply_act(v[i + 1], ACT) * scaled(int(u[j + i + 1]), s, s1.y);
+              v[i + 2] = apply_act(v[i + 2], ACT) * scaled(int(u[j + i + 2]), s, s1.z);
+              v[i + 3] = apply_act(v[i + 3], ACT) * scaled(int(u[j + i + 3]), s, s1.w);
             }
           }
-          if (L.type != kF32) flush_rows(out, L, m - lane, n0 + c, lane, p.vec);
+          uint4* o = reinterpret_cast<uint4*>(out + lane * kOutRow + (((c + j) * eb) & 63));
+          if (L.type == kF32) {
+            o[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            o[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+          } else {
+            o[0] = L.type == kBF16 ? make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                pack_bf16(v[6], v[7]))
+                                   : make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]),
+                                                pack_f16(v[6], v[7]));
+          }
         }
-        if (c + 64 >= out_n) break;
+      };
+      auto load = [&](uint32_t (&r)[16], uint32_t (&u)[16], int c) {
+        tmem_ld16(base + uint32_t(c), r);
+        if constexpr (GATED) tmem_ld16(base + uint32_t(out_n + c), u);
+      };
+      auto landed = [&](uint32_t (&r)[16], uint32_t (&u)[16]) {
+        wait16(r);
+        if constexpr (GATED) wait16(u);
+      };
+      auto all_read = [&]() {               // this warp's columns are in registers: the MMAs may have the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(mapa(smem_u32(&acc_empty[a]), 0));
+      };
+      int c = 32 * half;
+      if (c >= out_n) {
+        all_read();
+      } else {
+        uint32_t r0[16], u0[16], r1[16], u1[16];
+        load(r0, u0, c);
+#pragma unroll 1
+        for (; c < out_n; c += 64) {
+          landed(r0, u0);
+          load(r1, u1, c + 16);
+          work(r0, u0, c);
+          if (L.type == kF32) flush_rows(out, L, m, n0 + c, lane, p.vec);
+          landed(r1, u1);
+          if (c + 64 < out_n) load(r0, u0, c + 64);
+          else all_read();
+          work(r1, u1, c + 16);
+          flush_rows(out, L, m, n0 + (L.type == kF32 ? c + 16 : c), lane, p.vec);
+        }
       }
     }
   }
@@ -686,16 +740,16 @@ cudaError_t current_device(int* dev) {
   return *dev >= 0 && *dev < 64 ? cudaSuccess : cudaErrorInvalidDevice;
 }
 
-template <bool GATED>
+template <int ACT>
 cudaError_t allow_split(int dev) {
   static std::atomic<bool> set[64];
-  return allow_smem(gemm_i8_split_kernel<GATED>, kSmemMax - 4096, set, dev);
+  return allow_smem(gemm_i8_split_kernel<ACT>, kSmemMax - 4096, set, dev);
 }
 
 // How many clusters of ks CTAs of the split kernel, one CTA an SM, run at once:
 // fewer than the SMs divided by ks, as a cluster stays within one group of SMs
 // (16 clusters of 8 took two rounds: 14.0 us against 9.1 over 4).
-template <bool GATED>
+template <int ACT>
 int clusters_at_once(int dev, int ks) {
   static std::atomic<int> cached[64][kSplitMax + 1];
   int n = cached[dev][ks].load(std::memory_order_relaxed);
@@ -711,8 +765,8 @@ int clusters_at_once(int dev, int ks) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (allow_split<GATED>(dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, gemm_i8_split_kernel<GATED>, &cfg) != cudaSuccess || n < 1) {
+    if (allow_split<ACT>(dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, gemm_i8_split_kernel<ACT>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       return 1;
     }
@@ -735,8 +789,9 @@ struct SplitPlan {
 // tokens, 4096 x 4096: 11.0 us unsplit, 9.0 / 8.3 over 2 / 4 CTAs; 11008 x 4096:
 // 13.2 us in 86 tiles of 128 rows, 12.3 in 138 of 80; 16 tokens, 1024 x 8192
 // over 8 CTAs: 5.8 with 128 rows, 6.1 with 80.)
-template <bool GATED>
+template <int ACT>
 SplitPlan split_plan(const Linear& L, int dev) {
+  constexpr bool GATED = ACT != kNone;
   SplitPlan p = {};
   const int nsm = sm_count(dev);
   const int64_t kb = (L.K + kBK - 1) / kBK;
@@ -747,7 +802,7 @@ SplitPlan split_plan(const Linear& L, int dev) {
     for (int rows = 128; rows >= (c <= 2 ? 64 : 128); rows -= 16) {
       const int out_n = GATED ? rows / 2 : rows;
       const int64_t tn = (L.N + out_n - 1) / out_n, t = tn * p.tiles_m;
-      if (c > 1 && t > clusters_at_once<GATED>(dev, c)) break;
+      if (c > 1 && t > clusters_at_once<ACT>(dev, c)) break;
       const int64_t load = (c > 1 ? 1 : (t + nsm - 1) / nsm) * (rows + p.mt) * ((kb + c - 1) / c) +
                            250 * (c >= 8 ? 3 : c / 2);
       if (load < (rows < 128 ? p.load - p.load / 8 : p.load)) {
@@ -760,14 +815,15 @@ SplitPlan split_plan(const Linear& L, int dev) {
   return p;
 }
 
-template <bool GATED>
+template <int ACT>
 cudaError_t split(const Linear& L, cudaStream_t st) {
+  constexpr bool GATED = ACT != kNone;
   int dev;
   cudaError_t e = current_device(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = allow_split<GATED>(dev)) != cudaSuccess) return e;
+  if ((e = allow_split<ACT>(dev)) != cudaSuccess) return e;
   const int nsm = sm_count(dev);
-  const SplitPlan plan = split_plan<GATED>(L, dev);
+  const SplitPlan plan = split_plan<ACT>(L, dev);
   const int ks = plan.ks;
   if (plan.tiles_n > 0x7fffffff || plan.tiles_m > 65535) return cudaErrorInvalidValue;
   SplitArgs p;
@@ -800,7 +856,7 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<GATED>, p);
+  return cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<ACT>, p);
 }
 
 // Columns of a pair's tile: the fewest that one pair works through, counting a
@@ -828,24 +884,26 @@ int pair_columns(const Linear& L, int pairs) {
 // The split kernel has to be well ahead: measured, split / pair, 256 tokens,
 // 1024 x 8192 11.0 / 13.5 us, gated 1024 x 4096 9.1 / 11.7; 160 tokens, 256 x
 // 4096 6.3 / 8.5; but 512 tokens, 1024 x 4096 9.1 / 8.9, 160, 4096 x 4096 12.3 / 9.8.
-template <bool GATED>
+template <int ACT>
 bool prefer_split(const Linear& L, int dev) {
+  constexpr bool GATED = ACT != kNone;
   const int pairs = sm_count(dev) / 2, bn = pair_columns<GATED>(L, pairs), out_n = GATED ? bn / 2 : bn;
   const int64_t kb = (L.K + kBK - 1) / kBK;
   const int64_t rounds = ((L.M + 255) / 256 * ((L.N + out_n - 1) / out_n) + pairs - 1) / pairs;
   const int64_t stage = 128 + bn / 2 > bn * 7 / 4 ? 128 + bn / 2 : bn * 7 / 4;
   if (rounds > 1) return false;
-  const SplitPlan s = split_plan<GATED>(L, dev);
+  const SplitPlan s = split_plan<ACT>(L, dev);
   return 2 * (s.load + 14 * s.mt) < kb * stage + (GATED ? 4300 : 2800);
 }
 
-template <bool GATED>
+template <int ACT>
 cudaError_t pair(const Linear& L, cudaStream_t st) {
+  constexpr bool GATED = ACT != kNone;
   int dev;
   cudaError_t e = current_device(&dev);
   if (e != cudaSuccess) return e;
   static std::atomic<bool> set[64];
-  if ((e = allow_smem(gemm_i8_pair_kernel<GATED>, kPairRing + 1024, set, dev)) != cudaSuccess) return e;
+  if ((e = allow_smem(gemm_i8_pair_kernel<ACT>, kPairRing + 1024, set, dev)) != cudaSuccess) return e;
   const int pairs = sm_count(dev) / 2;
   PairArgs p;
   p.L = L;
@@ -875,23 +933,28 @@ cudaError_t pair(const Linear& L, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel<GATED>, p);
+  return cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel<ACT>, p);
+}
+
+template <int ACT>
+cudaError_t launch_as(const Linear& L, cudaStream_t st) {
+  if (L.M <= kSplitTokens) return split<ACT>(L, st);
+  int dev;
+  const cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  return prefer_split<ACT>(L, dev) ? split<ACT>(L, st) : pair<ACT>(L, st);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
-  const bool gated = L.act != kNone;
   if (L.M <= kGemvTokens) return launch_gemv(L, st);
-  bool few = L.M <= kSplitTokens;
-  if (!few) {
-    int dev;
-    const cudaError_t e = current_device(&dev);
-    if (e != cudaSuccess) return e;
-    few = gated ? prefer_split<true>(L, dev) : prefer_split<false>(L, dev);
+  switch (L.act) {
+    case kSilu: return launch_as<kSilu>(L, st);
+    case kGelu: return launch_as<kGelu>(L, st);
+    case kGeluTanh: return launch_as<kGeluTanh>(L, st);
+    default: return launch_as<kNone>(L, st);
   }
-  if (few) return gated ? split<true>(L, st) : split<false>(L, st);
-  return gated ? pair<true>(L, st) : pair<false>(L, st);
 }
 
 bool gemm_read_and_clear_timeout(cudaError_t* err) {
