@@ -37,14 +37,34 @@ struct Linear {
   int act;    // kNone: y is the product
 };
 
+// erfc(z) / exp(-z^2) / t, t = 1 / (1 + 0.4 z), for z in 0 .. 9.5: a polynomial of
+// degree 8 in t, fitted here (least squares over Chebyshev nodes, reweighted to
+// even the relative error out) to 6e-8.  Behind 9.5 exp(-z^2) is 0 in fp32.
+__device__ __forceinline__ float erfc_tail(float t) {
+  float p = 0.04026747867465019f;
+  p = fmaf(p, t, -0.13547100126743317f);
+  p = fmaf(p, t, 0.07384196668863297f);
+  p = fmaf(p, t, 0.09972977638244629f);
+  p = fmaf(p, t, 0.07150818407535553f);
+  p = fmaf(p, t, 0.19696307182312012f);
+  p = fmaf(p, t, 0.20095857977867126f);
+  p = fmaf(p, t, 0.22657571732997894f);
+  return fmaf(p, t, 0.22562630474567413f);
+}
+
 // act(g).  Forms without cancellation: for g << 0 the result keeps its
 // relative accuracy (1 + erf or 1 + tanh would lose it).  Where exp(-g) passes
 // 2^126 the quotient is 0, for a true |act| below |g| 2^-126.  The hardware's
-// exponential and division (2 + 1.2 |g| and 2 steps) stand for expf and the
-// IEEE division, whose instructions held up a gated tile's epilogue.
+// exponential and division (2 + 1.2 |g| and 2 steps) and the fit above stand for
+// expf, the IEEE division and erfcf, whose instructions held up a gated tile's
+// epilogue (gelu, 1228 x 1216 -> 12096: 51 us with erfcf).
 __device__ __forceinline__ float apply_act(float g, int act) {
   if (act == kSilu) return __fdividef(g, 1.0f + __expf(-g));
-  if (act == kGelu) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  if (act == kGelu) {
+    const float t = __fdividef(1.0f, fmaf(fabsf(g), 0.28284271247461900f, 1.0f));   // 0.4 |g| / sqrt 2
+    const float half = 0.5f * (__expf(-0.5f * (g * g)) * t) * erfc_tail(t);         // erfc(|g| / sqrt 2) / 2
+    return g * (g > 0.0f ? 1.0f - half : half);
+  }
   // g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)) = 0.5 g (1 + tanh(...))
   const float t = 1.5957691216057308f * (g + 0.044715f * g * g * g);
   return __fdividef(g, 1.0f + __expf(-t));

@@ -47,8 +47,10 @@ def gated_ref(accg, accu, xs, gs, us, act):
     at z = |g| / sqrt 2, one more for the factor g) and 1 + 3 |t| (gelu_tanh:
     |dt/t| <= 3 |dg/g|).  The activation itself, in units of U: the hardware's
     exponential of v, 2 + 1.173 |v| steps (the CUDA guide's bound) = 4 + 2.4 |v|,
-    the sum 1, its division 2 steps = 4, t's own evaluation 8 |t|; erfcf 4 steps
-    = 8, its argument 2 (1 + g^2), two products 2.  The product with u: 3 + 1.
+    the sum 1, its division 2 steps = 4, t's own evaluation 8 |t|; gelu's
+    erfc: the fit 1 (6e-8), its nine steps and three products 9 as simulated, t's
+    division 4, and exp(-g^2 / 2) 4 + 1.2 g^2, its argument's rounding g^2 / 2:
+    at most 18 + 2 g^2.  The product with u: 3 + 1.
     Far below zero the activation leaves fp32's normal range: where 1 + exp(-g)
     (or exp(-t)) passes 2^126 the hardware's quotient is 0, for a true |act| <
     |g| 2^-126, and one under 2^-126 may be flushed: together at most
@@ -63,7 +65,7 @@ def gated_ref(accg, accu, xs, gs, us, act):
         units = 3 * (1 + np.abs(g)) + 4 + 2.4 * np.abs(g) + 1 + 4
     elif act == "gelu":
         a = (0.5 * gt * t.special.erfc(-gt / math.sqrt(2.0))).numpy()
-        units = 3 * (2 + g * g) + 8 + 2 * (1 + g * g) + 2
+        units = 3 * (2 + g * g) + 18 + 2 * g * g
     else:
         tt = 2.0 * math.sqrt(2.0 / math.pi) * (g + 0.044715 * g ** 3)
         a = g / (1.0 + np.exp(-np.clip(tt, -700, 700)))

@@ -266,6 +266,25 @@ def _repack(t):
     return wide[:, :t.shape[1]]
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_activations_over_their_range(M, act):
+    """g on a fine grid (the gate's scales carry it), u = 1: the activation itself, fp32."""
+    g = np.concatenate([np.linspace(-13, 13, 20001), np.linspace(-1, 1, 4001), np.linspace(-120, 120, 4001),
+                        [0.0, -0.0, 1e-30, -1e-30, 1e-40, 3e4, -3e4]]).astype(np.float32)
+    N = len(g)
+    x = torch.zeros(M, 16, dtype=torch.int8, device="cuda")
+    x[:, 0] = 1
+    w = torch.zeros(N, 16, dtype=torch.int8, device="cuda")
+    w[:, 0] = 1
+    h = wq().wq_gated_i8(x, torch.ones(M, device="cuda"), w, torch.from_numpy(g).cuda(), w,
+                         torch.ones(N, device="cuda"), act=act, dtype=torch.float32)
+    one = np.ones((1, N))
+    ref, err = gated_ref(one, one, np.ones(1, np.float32), g, np.ones(N, np.float32), act)
+    assert_rounds_to(h[:1], ref, err, act)
+    assert torch.equal(h, h[:1].expand(M, N))
+
+
 def test_gated_zero_gate_and_saturated_gate():
     """g = 0 gives 0; a gate far below zero gives (a signed) 0, far above g u."""
     K, N = 64, 48
