@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
   __shared__ uint32_t tmem_slot, abort_word;
-  __shared__ float xscale[kSplitTokens];
+  __shared__ float xscale[kSplitTokens], wscale[128];
   volatile uint32_t* abort = &abort_word;
   const Linear& L = p.L;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -302,76 +302,102 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     if (elect_one()) commit_one(&done);   // always: the teardown waits on it before freeing tensor memory
   }
   __syncwarp();
-  // the scales of this thread's four outputs and of the tile's tokens, while
-  // the first operands are on their way
-  const int groups = out_n / 4, token0 = threadIdx.x / groups, tokens = kSplitThreads / groups;
-  const int j = threadIdx.x - token0 * groups;
-  const int64_t n = n0 + 4 * j;
-  const int left = token0 < tokens ? int(min(int64_t(4), L.N - n)) : 0;   // outputs of this thread inside the row
-  float s0[4], s1[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s0[i] = i < left ? L.s0[n + i] : 0.0f;
-    s1[i] = GATED && i < left ? L.s1[n + i] : 0.0f;
-  }
+  // the tile's scales, while the first operands are on their way
   const int mend = int(min(int64_t(mt), L.M - m0));     // tokens of this tile
+  const int row = 32 * (warp & 3) + lane;               // this lane's weight row, of tokens 32 (warp / 4) .. + 31 of 64
+  const int col = GATED && row >= out_n ? row - out_n : row;
+  const bool up = GATED && row >= out_n;
+  const int64_t n = n0 + col;
+  const float sw = row < p.rows && n < L.N ? (up ? L.s1[n] : L.s0[n]) : 0.0f;
   if (threadIdx.x < mend) xscale[threadIdx.x] = L.xs[m0 + threadIdx.x];
+  if (warp < 4) wscale[row] = sw;
   bool ok = wait_for(&done, 0, abort);
   ok = __all_sync(0xffffffffu, ok);   // tcgen05.ld needs the whole warp
+  const uint32_t tcol = tmem + (uint32_t(32 * (warp & 3)) << 16);
 
-  // The int32 sums as [rank][own token][128 rows]: with one rank in the idle
-  // ring (every MMA has read its operands and every copy has landed), with
-  // more behind the ring of each token's owner.
-  int* part = reinterpret_cast<int*>(ks > 1 ? ring + S * stage : ring);
-  const int own = mt / ks;             // tokens a rank owns
-  if (ks > 1) cluster_wait();
-  if (ok) {
-    tc_fence_after();
-    const uint32_t row = smem_u32(part) + uint32_t(32 * (warp & 3) + lane) * 4;
-    for (int c = 32 * (warp >> 2); c < mt; c += 64) {
-      uint32_t r[32];
-      tmem_ld32(tmem + (uint32_t(32 * (warp & 3)) << 16) + uint32_t(c), r);
-      tmem_wait_ld();
-      if (ks == 1) {
+  if (!GATED && ks == 1) {
+    // Unsplit: straight from tensor memory, neighbouring lanes to neighbouring
+    // outputs.  (Through shared memory, four outputs a thread, 128 tokens of 80
+    // rows took 3.8 us for this.)
+    __syncthreads();                    // xscale
+    if (ok) {
+      tc_fence_after();
+      for (int c = 32 * (warp >> 2); c < mend; c += 64) {
+        uint32_t r[32];
+        tmem_ld32(tcol + uint32_t(c), r);
+        tmem_wait_ld();
+        if (row < out_n && n < L.N) {
+          const int64_t at = (m0 + c) * L.ldy + n;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) part[(c + i) * 128 + 32 * (warp & 3) + lane] = int(r[i]);
-      } else {
-        // ks divides 32: token c + i belongs to rank i % ks
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          st_cluster(mapa(row + uint32_t(kr * own + (c + i) / ks) * 512, uint32_t(i & (ks - 1))), r[i]);
+          for (int i = 0; i < 32; ++i)
+            if (c + i < mend) store_one(L.y, at + i * L.ldy, scaled(int(r[i]), xscale[c + i], sw), L.type);
+        }
       }
     }
-  }
-  __syncthreads();
-  if (ks > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
-  // A thread takes four neighbouring outputs of a token; token t of this rank
-  // is row kr + ks t of the tile.
-  if (!*abort && left > 0) {
-    for (int t = token0; kr + ks * t < mend; t += tokens) {
-      int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  } else {
+    // The int32 sums as [rank][own token][128 rows]: gated with one rank, in the
+    // idle ring (every MMA has read its operands and every copy has landed);
+    // with more, behind the ring of each token's owner: token t belongs to rank
+    // t % ks (ks divides 32).
+    int* part = reinterpret_cast<int*>(ks > 1 ? ring + S * stage : ring);
+    const int own = mt / ks, lk = 31 - __clz(ks);
+    if (ks > 1) cluster_wait();
+    if (ok) {
+      tc_fence_after();
+      const uint32_t at = smem_u32(part) + uint32_t(kr * own * 128 + row) * 4;
+      for (int c = 32 * (warp >> 2); c < mt; c += 64) {
+        uint32_t r[32];
+        tmem_ld32(tcol + uint32_t(c), r);
+        tmem_wait_ld();
+        if (ks == 1) {
 #pragma unroll
-      for (int r = 0; r < kSplitMax; ++r)
-        if (r < ks) {
-          const int4 v = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + 4 * j);
-          a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
-          if constexpr (GATED) {
-            const int4 u = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + out_n + 4 * j);
-            b[0] += u.x; b[1] += u.y; b[2] += u.z; b[3] += u.w;
-          }
+          for (int i = 0; i < 32; ++i) part[(c + i) * 128 + row] = int(r[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            st_cluster(mapa(at + (uint32_t(c + i) >> lk) * 512, uint32_t(i & (ks - 1))), r[i]);
         }
-      const int m = kr + ks * t;
-      const float sx = xscale[m];
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = scaled(a[e], sx, s0[e]);
-        if constexpr (GATED) v[e] = apply_act(v[e], ACT) * scaled(b[e], sx, s1[e]);
       }
-      store_four(L.y, (m0 + m) * L.ldy + n, v, left, L.type, p.vec);
+    }
+    __syncthreads();
+    if (ks > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    // A thread takes four neighbouring outputs of a token; token t of this rank
+    // is token kr + ks t of the tile.
+    const int groups = out_n / 4, token0 = threadIdx.x / groups, tokens = kSplitThreads / groups;
+    const int j = threadIdx.x - token0 * groups;
+    const int left = token0 < tokens ? int(min(int64_t(4), L.N - n0 - 4 * j)) : 0;   // of them inside the row
+    if (!*abort && left > 0) {
+      float s0[4], s1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s0[i] = wscale[4 * j + i];
+        s1[i] = GATED ? wscale[out_n + 4 * j + i] : 0.0f;
+      }
+      for (int t = token0; kr + ks * t < mend; t += tokens) {
+        int a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < kSplitMax; ++r)
+          if (r < ks) {
+            const int4 v = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + 4 * j);
+            a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+            if constexpr (GATED) {
+              const int4 u = *reinterpret_cast<const int4*>(part + (r * own + t) * 128 + out_n + 4 * j);
+              b[0] += u.x; b[1] += u.y; b[2] += u.z; b[3] += u.w;
+            }
+          }
+        const int m = kr + ks * t;
+        const float sx = xscale[m];
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = scaled(a[e], sx, s0[e]);
+          if constexpr (GATED) v[e] = apply_act(v[e], ACT) * scaled(b[e], sx, s1[e]);
+        }
+        store_four(L.y, (m0 + m) * L.ldy + n0 + 4 * j, v, left, L.type, p.vec);
+      }
     }
   }
   tc_fence_before();
