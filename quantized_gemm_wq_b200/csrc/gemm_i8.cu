@@ -32,6 +32,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "i8.cuh"
 #include "wq_internal.cuh"
@@ -322,17 +323,22 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     __syncthreads();                    // xscale
     if (ok) {
       tc_fence_after();
-      for (int c = 32 * (warp >> 2); c < mend; c += 64) {
-        uint32_t r[32];
-        tmem_ld32(tcol + uint32_t(c), r);
-        tmem_wait_ld();
-        if (row < out_n && n < L.N) {
-          const int64_t at = (m0 + c) * L.ldy + n;
+      auto store = [&](auto type) {
+        for (int c = 32 * (warp >> 2); c < mend; c += 64) {
+          uint32_t r[32];
+          tmem_ld32(tcol + uint32_t(c), r);
+          tmem_wait_ld();
+          if (row < out_n && n < L.N) {
+            int64_t at = (m0 + c) * L.ldy + n;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < mend) store_one(L.y, at + i * L.ldy, scaled(int(r[i]), xscale[c + i], sw), L.type);
+            for (int i = 0; i < 32; ++i, at += L.ldy)
+              if (c + i < mend) store_one(L.y, at, scaled(int(r[i]), xscale[c + i], sw), decltype(type)::value);
+          }
         }
-      }
+      };
+      if (L.type == kBF16) store(std::integral_constant<int, kBF16>());
+      else if (L.type == kF16) store(std::integral_constant<int, kF16>());
+      else store(std::integral_constant<int, kF32>());
     }
   } else {
     // The int32 sums as [rank][own token][128 rows]: gated with one rank, in the
