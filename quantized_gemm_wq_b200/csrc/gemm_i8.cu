@@ -14,16 +14,16 @@
 //   when the tiles alone leave SMs idle: rank r owns the tokens r, r + ks, ...;
 //   every rank writes its int32 sums of them into the owner's shared memory,
 //   and after one cluster barrier the owner adds what it holds.
-//   Measured: 16 tokens 12288 -> 49152 93.8 us (6.46 TB/s), 64 tokens 4096 ->
-//   11008 12.4 us (3.8 TB/s: 3 us to the first data, 7.5 of stream, 2 of
-//   epilogue), gated 18.3 us.
+//   Measured: 16 tokens 12288 -> 49152 94 us (6.4 TB/s), 64 tokens 4096 -> 11008
+//   11.4 us (4.1 TB/s: 3 us to the first data, 7.5 of stream, 1 of epilogue),
+//   gated 18.5 us (4.9 TB/s).
 // pair kernel (larger batches): bound by the tensor cores.  Two SMs work on one
 //   tile of 256 tokens x BN weight rows (cta_group::2): each loads its 128
 //   tokens and half of the weight rows (gated: one SM the gate's, the other
 //   the up projection's), so a byte of shared memory feeds twice the MMAs.
 //   Persistent, two accumulators: a tile's epilogue runs beside the next
 //   tile's MMAs.  Measured: 2048 tokens 13824 -> 5120 92 us (3159 TOP/s), gated
-//   5120 -> 13824 173 us (3342 TOP/s); a stage of 128 bytes of K takes 513..530
+//   5120 -> 13824 171 us (3384 TOP/s); a stage of 128 bytes of K takes 513..530
 //   cycles at 256 columns, 512 of them the tensor pipe's.
 //
 // Every wait is bounded (bounded_wait.cuh): an expired wait raises this file's
@@ -780,7 +780,7 @@ cudaError_t allow_split(int dev) {
 
 // How many clusters of ks CTAs of the split kernel, one CTA an SM, run at once:
 // fewer than the SMs divided by ks, as a cluster stays within one group of SMs
-// (16 clusters of 8 took two rounds: 14.0 us against 9.1 over 4).
+// (16 clusters of 8 took two rounds: 13.1 us against 8.5 over 4).
 template <int ACT>
 int clusters_at_once(int dev, int ks) {
   static std::atomic<int> cached[64][kSplitMax + 1];
@@ -818,9 +818,9 @@ struct SplitPlan {
 // adds an exchange, as much as 250 of these for each doubling, and its clusters
 // have to be on the SMs at once, one CTA an SM; smaller tiles have to read a
 // good deal less to be worth it, and were not for clusters of 4 and 8.  (64
-// tokens, 4096 x 4096: 11.0 us unsplit, 9.0 / 8.3 over 2 / 4 CTAs; 11008 x 4096:
-// 13.2 us in 86 tiles of 128 rows, 12.3 in 138 of 80; 16 tokens, 1024 x 8192
-// over 8 CTAs: 5.8 with 128 rows, 6.1 with 80.)
+// tokens, 4096 x 4096: 9.5 us unsplit, 8.7 / 7.8 / 8.1 over 2 / 4 / 8 CTAs;
+// 11008 x 4096: 11.8 us in 86 tiles of 128 rows, 11.4 in 115 of 96, 14.1 in 172
+// halves of 128; 16 tokens, 1024 x 8192 over 8 CTAs: 5.5 with 128 rows, 5.9 with 80.)
 template <int ACT>
 SplitPlan split_plan(const Linear& L, int dev) {
   constexpr bool GATED = ACT != kNone;
@@ -914,8 +914,9 @@ int pair_columns(const Linear& L, int pairs) {
 // pair's stage takes its read or its MMAs (1.75 a column), its tile 2800 (gated
 // 4300) more than a split tile, which has an epilogue of its own of 14 a token.
 // The split kernel has to be well ahead: measured, split / pair, 256 tokens,
-// 1024 x 8192 11.0 / 13.5 us, gated 1024 x 4096 9.1 / 11.7; 160 tokens, 256 x
-// 4096 6.3 / 8.5; but 512 tokens, 1024 x 4096 9.1 / 8.9, 160, 4096 x 4096 12.3 / 9.8.
+// 1024 x 8192 9.9 / 13.2 us, gated 1024 x 4096 8.4 / 8.9; 160 tokens, 256 x 4096
+// 5.9 / 8.3; 146, 68 x 7554 7.3 / 16.9; but 512 tokens, 1024 x 4096 8.3 / 8.6,
+// 160, 4096 x 4096 11.0 / 9.5.
 template <int ACT>
 bool prefer_split(const Linear& L, int dev) {
   constexpr bool GATED = ACT != kNone;
