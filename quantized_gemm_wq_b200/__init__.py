@@ -272,6 +272,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
 _empty_strided = torch.empty_strided
 _INT8, _FP32 = torch.int8, torch.float32
+_lib_quantize_i8, _lib_gemm_i8, _lib_gated_i8 = lib.wq_quantize_i8, lib.wq_gemm_i8, lib.wq_gated_i8
 
 
 def _need_matrix(t: torch.Tensor, what: str, dtypes=(_INT8,), dev=None) -> None:
@@ -293,34 +294,22 @@ def _pad16(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
-def _run(fn, where: str, dev: int, stream, args) -> None:
-    """fn(*args, stream) with `dev` current, on its current stream when `stream` is None."""
+def _elsewhere(call, dev: int, stream, *args):
+    """call(*args) with `dev` current and, if one is given, on `stream` (so that what
+    the call allocates is the stream's too)."""
     if stream is not None and stream.device.index != dev:
         raise ValueError("stream must be one of the operands' device")
-    if dev == _current_device():
-        st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st != WQ_OK:
-        raise WQError(st, where)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(*args)
 
 
-def _empty(size, strides, dtype, x, stream):
-    """Uninitialised memory on x's device, of the stream that will write it."""
-    if stream is None:
-        return _empty_strided(size, strides, dtype=dtype, device=x.device)
-    with torch.cuda.stream(stream):
-        return _empty_strided(size, strides, dtype=dtype, device=x.device)
-
-
-def _output(y, M: int, N: int, dtype, x, stream):
-    """The output (made on x's device if None), its row stride and its wq_type."""
+def _output(y, M: int, N: int, dtype, x):
+    """The given output's row stride and wq_type; or a new one on x's device, and its."""
     if y is None:
         yt = _TYPES.get(dtype)
         if yt is None:
             raise ValueError("dtype must be torch.bfloat16, torch.float16 or torch.float32")
-        return _empty((M, N), (N, 1), dtype, x, stream), N, yt
+        return _empty_strided((M, N), (N, 1), dtype=dtype, device=x.device), N, yt
     _need_matrix(y, "the output", tuple(_TYPES), x.get_device())
     if y.shape != (M, N):
         raise ValueError(f"the output must be [{M}, {N}]")
@@ -335,6 +324,8 @@ def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
     xt, dev = _TYPES.get(x.dtype), x.get_device()
     if xt is None or dev < 0 or x.dim() != 2:
         _need_matrix(x, "x", tuple(_TYPES))
+    if stream is not None or dev != _current_device():
+        return _elsewhere(wq_quantize_i8, dev, stream, x, codes, scales)
     R, K = x.shape
     ldx, step = x.stride()
     if step != 1:
@@ -343,18 +334,20 @@ def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
         # rows on 32 bytes, L2's sectors: the tensor-core kernels take a quarter
         # longer where they are on 16 (2048 x 5120 -> 5120: 48 against 38 us)
         ldc = (K + 31) // 32 * 32
-        codes = _empty((R, K), (ldc, 1), _INT8, x, stream)
+        codes = _empty_strided((R, K), (ldc, 1), dtype=_INT8, device=x.device)
     else:
         _need_matrix(codes, "codes", dev=dev)
         if codes.shape != x.shape:
             raise ValueError("codes must have x's shape")
         ldc = codes.stride(0) if R > 1 else _pad16(K)
     if scales is None:
-        scales = _empty((R,), (1,), _FP32, x, stream)
+        scales = _empty_strided((R,), (1,), dtype=_FP32, device=x.device)
     else:
         _need_scales(scales, R, dev, "scales")
-    _run(lib.wq_quantize_i8, "wq_quantize_i8", dev, stream,
-         (x.data_ptr(), xt, R, K, ldx if R > 1 else K, codes.data_ptr(), ldc, scales.data_ptr()))
+    st = _lib_quantize_i8(x.data_ptr(), xt, R, K, ldx if R > 1 else K, codes.data_ptr(), ldc, scales.data_ptr(),
+                          _raw_stream(dev))
+    if st != WQ_OK:
+        raise WQError(st, "wq_quantize_i8")
     return codes, scales
 
 
@@ -364,13 +357,15 @@ def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     codes ``x`` [M, K] and ``w`` [N, K] -> ``y`` [M, N] of ``dtype`` (or the
     given ``y``'s type).  Row strides of codes are multiples of 16."""
     dev = x.get_device()
-    if x.dim() != 2 or w.dim() != 2:
+    if x.dim() != 2 or w.dim() != 2 or dev < 0:
         raise ValueError("x and w must be 2-D CUDA tensors")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(wq_gemm_i8, dev, stream, x, x_scales, w, w_scales, y, dtype)
     M, K = x.shape
     N, Kw = w.shape
     ldx, xstep = x.stride()
     ldw, wstep = w.stride()
-    if not (x.dtype is _INT8 and w.dtype is _INT8 and K == Kw and xstep == 1 and wstep == 1 and dev >= 0
+    if not (x.dtype is _INT8 and w.dtype is _INT8 and K == Kw and xstep == 1 and wstep == 1
             and w.get_device() == dev and x_scales.dtype is _FP32 and w_scales.dtype is _FP32
             and x_scales.shape == (M,) and w_scales.shape == (N,) and x_scales.get_device() == dev
             and w_scales.get_device() == dev and x_scales.is_contiguous() and w_scales.is_contiguous()):
@@ -380,10 +375,11 @@ def wq_gemm_i8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
             raise ValueError("w must be [N, K] with x's K")
         _need_scales(x_scales, M, dev, "x_scales")
         _need_scales(w_scales, N, dev, "w_scales")
-    y, ldy, yt = _output(y, M, N, dtype, x, stream)
-    _run(lib.wq_gemm_i8, "wq_gemm_i8", dev, stream,
-         (x.data_ptr(), ldx if M > 1 else _pad16(K), x_scales.data_ptr(), M, N, K, w.data_ptr(),
-          ldw if N > 1 else _pad16(K), w_scales.data_ptr(), y.data_ptr(), yt, ldy))
+    y, ldy, yt = _output(y, M, N, dtype, x)
+    st = _lib_gemm_i8(x.data_ptr(), ldx if M > 1 else _pad16(K), x_scales.data_ptr(), M, N, K, w.data_ptr(),
+                      ldw if N > 1 else _pad16(K), w_scales.data_ptr(), y.data_ptr(), yt, ldy, _raw_stream(dev))
+    if st != WQ_OK:
+        raise WQError(st, "wq_gemm_i8")
     return y
 
 
@@ -397,14 +393,16 @@ def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, g
     if at is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     dev = x.get_device()
-    if x.dim() != 2 or w_gate.dim() != 2 or w_up.dim() != 2:
+    if x.dim() != 2 or w_gate.dim() != 2 or w_up.dim() != 2 or dev < 0:
         raise ValueError("x, w_gate and w_up must be 2-D CUDA tensors")
+    if stream is not None or dev != _current_device():
+        return _elsewhere(wq_gated_i8, dev, stream, x, x_scales, w_gate, gate_scales, w_up, up_scales, act, h, dtype)
     M, K = x.shape
     N, Kw = w_gate.shape
     ldx, xstep = x.stride()
     strides = ldw, wstep = w_gate.stride()
     if not (x.dtype is _INT8 and w_gate.dtype is _INT8 and w_up.dtype is _INT8 and K == Kw and xstep == 1
-            and wstep == 1 and w_up.shape == w_gate.shape and w_up.stride() == strides and dev >= 0
+            and wstep == 1 and w_up.shape == w_gate.shape and w_up.stride() == strides
             and w_gate.get_device() == dev and w_up.get_device() == dev and x_scales.dtype is _FP32
             and gate_scales.dtype is _FP32 and up_scales.dtype is _FP32 and x_scales.shape == (M,)
             and gate_scales.shape == (N,) and up_scales.shape == (N,) and x_scales.get_device() == dev
@@ -418,9 +416,10 @@ def wq_gated_i8(x: torch.Tensor, x_scales: torch.Tensor, w_gate: torch.Tensor, g
         _need_scales(x_scales, M, dev, "x_scales")
         _need_scales(gate_scales, N, dev, "gate_scales")
         _need_scales(up_scales, N, dev, "up_scales")
-    h, ldh, ht = _output(h, M, N, dtype, x, stream)
-    _run(lib.wq_gated_i8, "wq_gated_i8", dev, stream,
-         (x.data_ptr(), ldx if M > 1 else _pad16(K), x_scales.data_ptr(), M, N, K, w_gate.data_ptr(),
-          gate_scales.data_ptr(), w_up.data_ptr(), up_scales.data_ptr(), ldw if N > 1 else _pad16(K), at,
-          h.data_ptr(), ht, ldh))
+    h, ldh, ht = _output(h, M, N, dtype, x)
+    st = _lib_gated_i8(x.data_ptr(), ldx if M > 1 else _pad16(K), x_scales.data_ptr(), M, N, K, w_gate.data_ptr(),
+                       gate_scales.data_ptr(), w_up.data_ptr(), up_scales.data_ptr(), ldw if N > 1 else _pad16(K),
+                       at, h.data_ptr(), ht, ldh, _raw_stream(dev))
+    if st != WQ_OK:
+        raise WQError(st, "wq_gated_i8")
     return h
