@@ -16,7 +16,7 @@
 //   and after one cluster barrier the owner adds what it holds.
 //   Measured: 16 tokens 12288 -> 49152 94 us (6.4 TB/s), 64 tokens 4096 -> 11008
 //   11.4 us (4.1 TB/s: 3 us to the first data, 7.5 of stream, 1 of epilogue),
-//   gated 18.5 us (4.9 TB/s).
+//   gated 18.0 us (5.0 TB/s).
 // pair kernel (larger batches): bound by the tensor cores.  Two SMs work on one
 //   tile of 256 tokens x BN weight rows (cta_group::2): each loads its 128
 //   tokens and half of the weight rows (gated: one SM the gate's, the other
@@ -204,7 +204,7 @@ __device__ __forceinline__ void store_four(void* y, int64_t i, const float (&v)[
 struct alignas(64) SplitArgs {
   CUtensorMap tx, t0, t1;
   Linear L;
-  int rows;      // weight rows of a tile, a multiple of 16; the MMA's rows behind them are idle
+  int rows;      // weight rows of a tile, a multiple of 16, at least kSplitRowsMin; the MMA's rows behind them are idle
   int mt;        // tokens of a tile: a multiple of 32, at most kSplitTokens
   int stages;
   int vec;       // rows of y start where a store of four outputs may
@@ -213,7 +213,12 @@ struct alignas(64) SplitArgs {
 constexpr int kSplitThreads = 256;
 constexpr int kSplitTokens = 128;
 constexpr int kSplitMax = 8;            // CTAs of a cluster along K
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 12;
+constexpr int kSplitRowsMin = 64;
+// Stages hold a tile's own rows, no room for the MMA's others: more of them fit
+// (128 tokens 4096 -> 11008 13.6 -> 13.1 us, gated 64 tokens 18.7 -> 18.0).  For
+// the idle rows the MMA reads on into what follows, this far at most.
+constexpr uint32_t kSplitSlack = (128 - kSplitRowsMin) * kBK;
 
 template <int ACT>
 __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const __grid_constant__ SplitArgs p) {
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   const Linear& L = p.L;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int S = p.stages, mt = p.mt;
-  const uint32_t stage = kTile + uint32_t(mt) * kBK;
+  const uint32_t wtile = uint32_t(p.rows) * kBK, stage = wtile + uint32_t(mt) * kBK;
   const int ks = gridDim.y, kr = blockIdx.y;
   const int kb_all = int((L.K + kBK - 1) / kBK);
   const int kb0 = int(int64_t(kb_all) * kr / ks), nkb = int(int64_t(kb_all) * (kr + 1) / ks) - kb0;
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
         mbar_expect_tx(&full[at.s], uint32_t(p.rows + mt) * kBK);
         tma_load_2d(w, &p.t0, &full[at.s], k, int(n0));
         if constexpr (GATED) tma_load_2d(w + out_n * kBK, &p.t1, &full[at.s], k, int(n0));
-        tma_load_2d(w + kTile, &p.tx, &full[at.s], k, int(m0));
+        tma_load_2d(w + wtile, &p.tx, &full[at.s], k, int(m0));
       }
       ++issued;
     }
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     for (int i = 0; i < nkb; ++i, at.next(S)) {
       if (!__all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort))) break;
       tc_fence_after();
-      const uint64_t a = ring_desc + uint32_t(at.s) * (stage >> 4), b = a + (kTile >> 4);
+      const uint64_t a = ring_desc + uint32_t(at.s) * (stage >> 4), b = a + (wtile >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk)
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     // idle ring (every MMA has read its operands and every copy has landed);
     // with more, behind the ring of each token's owner: token t belongs to rank
     // t % ks (ks divides 32).
-    int* part = reinterpret_cast<int*>(ks > 1 ? ring + S * stage : ring);
+    int* part = reinterpret_cast<int*>(ks > 1 ? ring + S * stage + kSplitSlack : ring);
     const int own = mt / ks, lk = 31 - __clz(ks);
     if (ks > 1) cluster_wait();
     if (ok) {
@@ -831,7 +836,7 @@ SplitPlan split_plan(const Linear& L, int dev) {
   p.tiles_m = (L.M + p.mt - 1) / p.mt;
   p.load = INT64_MAX;
   for (int c = 1; c <= kSplitMax && (c == 1 || kb >= 2 * c); c *= 2)
-    for (int rows = 128; rows >= (c <= 2 ? 64 : 128); rows -= 16) {
+    for (int rows = 128; rows >= (c <= 2 ? kSplitRowsMin : 128); rows -= 16) {
       const int out_n = GATED ? rows / 2 : rows;
       const int64_t tn = (L.N + out_n - 1) / out_n, t = tn * p.tiles_m;
       if (c > 1 && t > clusters_at_once<ACT>(dev, c)) break;
@@ -864,7 +869,7 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   p.rows = plan.rows;
   const int eb = type_bytes(L.type);
   p.vec = reinterpret_cast<uintptr_t>(L.y) % (4 * eb) == 0 && (L.ldy * eb) % (4 * eb) == 0;
-  const uint32_t stage = kTile + uint32_t(p.mt) * kBK;
+  const uint32_t stage = uint32_t(p.rows + p.mt) * kBK;
   const int out_n = GATED ? p.rows / 2 : p.rows;
   if (!make_map(&p.tx, L.x, L.K, L.M, L.ldx, p.mt) || !make_map(&p.t0, L.w0, L.K, L.N, L.ldw, out_n) ||
       (GATED && !make_map(&p.t1, L.w1, L.K, L.N, L.ldw, out_n)))
@@ -872,12 +877,12 @@ cudaError_t split(const Linear& L, cudaStream_t st) {
   const uint32_t parked = ks > 1 ? uint32_t(p.mt) * 512 : 0;
   // two CTAs an SM where there are more than SMs, else one with a deeper ring
   const uint32_t budget = (plan.tiles_n * plan.tiles_m * ks > nsm ? kSmemMax / 2 : kSmemMax) - 4096;
-  p.stages = int((budget - 1024 - parked) / stage);
+  p.stages = int((budget - 1024 - kSplitSlack - parked) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(plan.tiles_n), unsigned(ks), unsigned(plan.tiles_m));
   cfg.blockDim = dim3(kSplitThreads, 1, 1);
-  cfg.dynamicSmemBytes = p.stages * stage + parked + 1024;
+  cfg.dynamicSmemBytes = p.stages * stage + kSplitSlack + parked + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
