@@ -42,14 +42,14 @@ struct Linear {
 // even the relative error out) to 6e-8.  Behind 9.5 exp(-z^2) is 0 in fp32.
 __device__ __forceinline__ float erfc_tail(float t) {
   float p = 0.04026747867465019f;
-  p = fmaf(p, t, -0.13547100126743317f);
-  p = fmaf(p, t, 0.07384196668863297f);
-  p = fmaf(p, t, 0.09972977638244629f);
-  p = fmaf(p, t, 0.07150818407535553f);
-  p = fmaf(p, t, 0.19696307182312012f);
-  p = fmaf(p, t, 0.20095857977867126f);
-  p = fmaf(p, t, 0.22657571732997894f);
-  return fmaf(p, t, 0.22562630474567413f);
+  p = __fmaf_rn(p, t, -0.13547100126743317f);
+  p = __fmaf_rn(p, t, 0.07384196668863297f);
+  p = __fmaf_rn(p, t, 0.09972977638244629f);
+  p = __fmaf_rn(p, t, 0.07150818407535553f);
+  p = __fmaf_rn(p, t, 0.19696307182312012f);
+  p = __fmaf_rn(p, t, 0.20095857977867126f);
+  p = __fmaf_rn(p, t, 0.22657571732997894f);
+  return __fmaf_rn(p, t, 0.22562630474567413f);
 }
 
 // act(g).  Forms without cancellation: for g << 0 the result keeps its
@@ -58,22 +58,27 @@ __device__ __forceinline__ float erfc_tail(float t) {
 // exponential and division (2 + 1.2 |g| and 2 steps) and the fit above stand for
 // expf, the IEEE division and erfcf, whose instructions held up a gated tile's
 // epilogue (gelu, 1228 x 1216 -> 12096: 51 us with erfcf).
+// Every rounding is spelled out: of plain products and sums the compiler may
+// contract others in each kernel, and a token's bits would depend on its batch.
 __device__ __forceinline__ float apply_act(float g, int act) {
-  if (act == kSilu) return __fdividef(g, 1.0f + __expf(-g));
+  if (act == kSilu) return __fdividef(g, __fadd_rn(1.0f, __expf(-g)));
   if (act == kGelu) {
-    const float t = __fdividef(1.0f, fmaf(fabsf(g), 0.28284271247461900f, 1.0f));   // 0.4 |g| / sqrt 2
-    const float half = 0.5f * (__expf(-0.5f * (g * g)) * t) * erfc_tail(t);         // erfc(|g| / sqrt 2) / 2
-    return g * (g > 0.0f ? 1.0f - half : half);
+    const float t = __fdividef(1.0f, __fmaf_rn(fabsf(g), 0.28284271247461900f, 1.0f));          // 0.4 |g| / sqrt 2
+    const float e = __expf(__fmul_rn(-0.5f, __fmul_rn(g, g)));
+    const float half = __fmul_rn(0.5f, __fmul_rn(__fmul_rn(e, t), erfc_tail(t)));               // erfc(|g| / sqrt 2) / 2
+    return __fmul_rn(g, g > 0.0f ? __fsub_rn(1.0f, half) : half);
   }
-  // g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)) = 0.5 g (1 + tanh(...))
-  const float t = 1.5957691216057308f * (g + 0.044715f * g * g * g);
-  return __fdividef(g, 1.0f + __expf(-t));
+  // g sigmoid(t) = 0.5 g (1 + tanh(t / 2)), t = 2 sqrt(2/pi) (g + 0.044715 g^3) = g (K + 0.044715 K g^2)
+  const float t = __fmul_rn(g, __fmaf_rn(0.07135481627260025f, __fmul_rn(g, g), 1.5957691216057308f));
+  return __fdividef(g, __fadd_rn(1.0f, __expf(-t)));
 }
 
 // acc s_x s_w, scaled in that order: s_x s_w alone could leave fp32's range
 // where the result does not.  acc above 2^24 is rounded to fp32 (half a step,
 // 2^-24), as each of the two products is.
-__device__ __forceinline__ float scaled(int acc, float sx, float sw) { return float(acc) * sx * sw; }
+__device__ __forceinline__ float scaled(int acc, float sx, float sw) {
+  return __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
+}
 
 __device__ __forceinline__ void store_one(void* y, int64_t i, float v, int type) {
   if (type == kBF16)

@@ -1,0 +1,68 @@
+"""The activations of wq_gated_i8 by themselves: the gate's scales carry g exactly
+(one product of 1 and 1), u = 1, so h is act(g) and nothing else is rounded."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from i8_util import codes, scales, wq
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ["silu", "gelu", "gelu_tanh"]
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def _act(g, act, M, dtype):
+    """h of M equal tokens for the gate values g."""
+    N = len(g)
+    x = torch.zeros(M, 16, dtype=torch.int8, device="cuda")
+    x[:, 0] = 1
+    w = torch.zeros(N, 16, dtype=torch.int8, device="cuda")
+    w[:, 0] = 1
+    return wq().wq_gated_i8(x, torch.ones(M, device="cuda"), w, torch.from_numpy(g).cuda(), w,
+                            torch.ones(N, device="cuda"), act=act, dtype=dtype)
+
+
+def _grid():
+    return np.concatenate([np.linspace(-16, 16, 30011), np.linspace(-1, 1, 4001), np.linspace(-130, -60, 9001),
+                           np.linspace(-120, 120, 4001), np.geomspace(1e-38, 1e38, 2001), -np.geomspace(1e-38, 1e38, 2001),
+                           [0.0, -0.0, 1e-42, -1e-42]]).astype(np.float32)
+
+
+# tokens for each kernel: warp MMAs, split (one and three token tiles of 32), pair
+KERNELS = [1, 8, 9, 40, 96, 128, 300]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_is_one_function_in_every_kernel(act, dtype):
+    """The same gate values through every kernel: the same bits, one token or 300."""
+    g = _grid()
+    want = _act(g, act, 1, dtype)
+    for M in KERNELS[1:]:
+        h = _act(g, act, M, dtype)
+        assert torch.equal(h.view(torch.int16 if dtype != torch.float32 else torch.int32),
+                           want.expand(M, -1).contiguous().view(torch.int16 if dtype != torch.float32 else torch.int32)), M
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_rows_do_not_depend_on_the_batch(act, dtype):
+    """The same tokens, alone and in batches that other kernels take: the same bits."""
+    rng = np.random.default_rng(12)
+    N, K = 1300, 333
+    x, _ = codes(rng, 600, K)
+    xs, _ = scales(rng, 600)
+    w, _ = codes(rng, N, K)
+    ws, _ = scales(rng, N)
+    u, _ = codes(rng, N, K)
+    us, _ = scales(rng, N)
+    ws *= 1.0 / (74.0 ** 2 * K ** 0.5 * 1e-3)           # gate values of unit size, and their spread
+    us *= 1e-3
+    full = wq().wq_gated_i8(x, xs, w, ws, u, us, act=act, dtype=dtype)
+    assert torch.isfinite(full).all() and (full != 0).float().mean() > 0.5
+    for m in (1, 2, 8, 9, 16, 33, 64, 128, 129, 257):
+        h = wq().wq_gated_i8(x[5:5 + m], xs[5:5 + m], w, ws, u, us, act=act, dtype=dtype)
+        assert torch.equal(h, full[5:5 + m]), m
