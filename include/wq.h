@@ -314,6 +314,16 @@ wq_status wq_gemm_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_
  * projection's weights, each as in wq_gemm_i8, kept in fp32 up to the one
  * rounding of h to h_type.
  *
+ * act(g) is evaluated in fp32.  Its own error, in units of 2^-24 of its value,
+ * is at most (t = 2 sqrt(2/pi) (g + 0.044715 g^3), the hardware's 2^x and 1 / x
+ * within their documented steps)
+ *                      silu           gelu            gelu_tanh
+ *   h in fp32          9              18 + 0.5 g^2    9 + 4 |t|
+ *   h in bf16, fp16    9 + 2.4 |g|    18 + 1.7 g^2    9 + 6.4 |t|
+ * below 0 (above it, with |g|, g^2 / 2 and |t| put at 1), down to where the value
+ * leaves fp32's normal range, 2^-126; under that it is within 2^-140.  act of
+ * minus infinity is NaN.
+ *
  *   w_gate, w_up   in   int8 [N, K], both with row stride ldw; scales fp32 [N]
  *   act                 the gate's activation
  *   h              out  h_type [M, N], row stride ldh

@@ -987,11 +987,14 @@ cudaError_t launch_as(const Linear& L, cudaStream_t st) {
 
 cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
   if (L.M <= kGemvTokens) return launch_gemv(L, st);
-  switch (L.act) {
+  if (L.act == kNone) return launch_as<kNone>(L, st);
+  switch (L.type == kF32 ? L.act + kFull : L.act) {
     case kSilu: return launch_as<kSilu>(L, st);
     case kGelu: return launch_as<kGelu>(L, st);
     case kGeluTanh: return launch_as<kGeluTanh>(L, st);
-    default: return launch_as<kNone>(L, st);
+    case kSilu + kFull: return launch_as<kSilu + kFull>(L, st);
+    case kGelu + kFull: return launch_as<kGelu + kFull>(L, st);
+    default: return launch_as<kGeluTanh + kFull>(L, st);
   }
 }
 

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) gemv_i8_kernel(const Linear L)
         for (int r = 0; r < RT; ++r) s[r] += red[w][r][m][row];
       const float sx = L.xs[m];
       float v = scaled(s[0], sx, L.s0[n]);
-      if constexpr (GATED) v = apply_act(v, L.act) * scaled(s[1], sx, L.s1[n]);
+      if constexpr (GATED) v = apply_act(v, L.type == kF32 ? L.act + kFull : L.act) * scaled(s[1], sx, L.s1[n]);
       store_one(L.y, m * L.ldy + n, v, L.type);
     }
   }

@@ -19,6 +19,7 @@ namespace i8 {
 
 enum Type { kBF16 = 0, kF16 = 1, kF32 = 2 };                  // wq_type
 enum Act { kSilu = 0, kGelu = 1, kGeluTanh = 2, kNone = -1 };  // wq_act; kNone: no gate
+constexpr int kFull = 4;   // added to an activation: the form for an fp32 result
 
 inline int type_bytes(int t) { return t == kF32 ? 4 : 2; }
 
@@ -54,25 +55,57 @@ __device__ __forceinline__ float erfc_tail(float t) {
   return __fmaf_rn(p, t, 0.27077242732048035f);
 }
 
-// act(g).  Forms without cancellation: for g << 0 the result keeps its
-// relative accuracy (1 + erf or 1 + tanh would lose it).  Where exp(-g) passes
-// 2^126 the quotient is 0, for a true |act| below |g| 2^-126.  The hardware's
-// exponential and division (2 + 1.2 |g| and 2 steps) and the fit above stand for
-// expf, the IEEE division and erfcf, whose instructions held up a gated tile's
-// epilogue (gelu, 1228 x 1216 -> 12096: 51 us with erfcf).
+// The hardware's 2^x (2 steps) and 1 / x (1 step).
+__device__ __forceinline__ float hw_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float hw_reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The activations keep their relative accuracy for g << 0 (forms with 1 + erf or
+// 1 + tanh would lose it there) until they leave fp32's normal range; their
+// errors are stated at wq_gated_i8 (wq.h).
+// FULL, for an fp32 result: CUDA's expf.  Else the hardware's 2^x of a rounded
+// argument, whose error grows with it by 1.2 steps a unit: at its far end a
+// fiftieth of the half step that bf16's rounding may take, a seventh of fp16's, and
+// a gated tile's epilogue waits for these instructions (1228 x 1216 -> 12096 to
+// bf16: silu 33.1 us, with expf 35.1; gelu 37.0 and 38.6).
 // Every rounding is spelled out: of plain products and sums the compiler may
 // contract others in each kernel, and a token's bits would depend on its batch.
-__device__ __forceinline__ float apply_act(float g, int act) {
-  if (act == kSilu) return __fdividef(g, __fadd_rn(1.0f, __expf(-g)));
+
+// g sigmoid(v) by e = exp(-|v|) <= 1: g / (1 + e) above zero, g e / (1 + e)
+// below, so that nothing overflows.  Below -64 the sum is 1, and e is taken 64
+// further up (2^64, e^64), clear of the subnormals; the last product undoes it.
+template <bool FULL>
+__device__ __forceinline__ float gate_of(float g, float v) {
+  const bool far = v < -64.0f;
+  float e;
+  if constexpr (FULL) e = expf(__fsub_rn(far ? 64.0f : 0.0f, fabsf(v)));     // exact for 32 <= |v| <= 128
+  else e = hw_exp2(__fmaf_rn(fabsf(v), -1.4426950408889634f, far ? 64.0f : 0.0f));
+  const float q = hw_reciprocal(__fadd_rn(1.0f, e)), down = FULL ? 1.6038108905486378e-28f : 0x1p-64f;   // exp(-64)
+  return __fmul_rn(v > 0.0f ? g : __fmul_rn(g, e), far ? down : q);
+}
+
+template <bool FULL>
+__device__ __forceinline__ float act_of(float g, int act) {
+  if (act == kSilu) return gate_of<FULL>(g, g);
   if (act == kGelu) {
-    const float t = __fdividef(1.0f, __fmaf_rn(fabsf(g), 0.33941125496954283f, 1.0f));          // 0.48 |g| / sqrt 2
-    const float e = __expf(__fmul_rn(-0.5f, __fmul_rn(g, g)));
-    const float half = __fmul_rn(0.5f, __fmul_rn(__fmul_rn(e, t), erfc_tail(t)));               // erfc(|g| / sqrt 2) / 2
+    const float t = hw_reciprocal(__fmaf_rn(fabsf(g), 0.33941125496954283f, 1.0f));   // 0.48 |g| / sqrt 2
+    const float x = __fmul_rn(-0.5f, __fmul_rn(g, g)), e = FULL ? expf(x) : __expf(x);
+    const float half = __fmul_rn(0.5f, __fmul_rn(__fmul_rn(e, t), erfc_tail(t)));     // erfc(|g| / sqrt 2) / 2
     return __fmul_rn(g, g > 0.0f ? __fsub_rn(1.0f, half) : half);
   }
-  // g sigmoid(t) = 0.5 g (1 + tanh(t / 2)), t = 2 sqrt(2/pi) (g + 0.044715 g^3) = g (K + 0.044715 K g^2)
-  const float t = __fmul_rn(g, __fmaf_rn(0.07135481627260025f, __fmul_rn(g, g), 1.5957691216057308f));
-  return __fdividef(g, __fadd_rn(1.0f, __expf(-t)));
+  // 0.5 g (1 + tanh(t / 2)) = g sigmoid(t), t = 2 sqrt(2/pi) (g + 0.044715 g^3) = g (c + 0.044715 c g^2)
+  return gate_of<FULL>(g, __fmul_rn(g, __fmaf_rn(0.07135481627260025f, __fmul_rn(g, g), 1.5957691216057308f)));
+}
+// act: an Act, with kFull added for an fp32 result.
+__device__ __forceinline__ float apply_act(float g, int act) {
+  return act >= kFull ? act_of<true>(g, act - kFull) : act_of<false>(g, act);
 }
 
 // acc s_x s_w, scaled in that order: s_x s_w alone could leave fp32's range
