@@ -1,10 +1,12 @@
 """Build ``libwq.so`` (the C-ABI library) in-tree with nvcc for sm_100a.
 
 A second build, ``libwq_shortwait.so``, compiles the same sources with a
-pipeline-wait limit of 0 (``WQ_PIPE_WAIT_NS``) and the test hook
-``wq_test_expire_wait`` (``WQ_TEST_HOOKS``): a kernel whose bounded wait is on
-a barrier nothing arrives on.  Only the tests load it, to check that an
-expired wait is reported as WQ_ERR_DEVICE_TIMEOUT and leaves the GPU usable.
+pipeline-wait limit of 0 (``WQ_PIPE_WAIT_NS``) and two test hooks
+(``WQ_TEST_HOOKS``): ``wq_test_expire_wait``, a kernel whose bounded wait is on
+a barrier nothing arrives on, and ``wq_test_give_up_i8``, which makes one chosen
+wait of the 8-bit tensor-core kernels give up.  Only the tests load it, to check
+that an expired wait is reported as WQ_ERR_DEVICE_TIMEOUT and leaves the GPU
+usable.
 
 Each ``csrc/*.cu`` translation unit is compiled for ``sm_100a`` only, the CUDA
 runtime is linked statically and the CUDA driver API is reached at run time

@@ -128,7 +128,34 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile uint32_t* abort) {
+// The waits of both kernels, for the test hook: a slot that may be filled again, a
+// slot that is full, a final accumulator, an accumulator that has been read.
+enum Wait { kWaitEmpty, kWaitFull, kWaitDone, kWaitAccEmpty };
+#ifdef WQ_TEST_HOOKS
+// Test builds: the wait that gives up at once, {which, its cluster, the CTA's rank
+// in it, how many such waits before it}; none where the first is negative.
+__device__ int g_give_up[4] = {-1, 0, 0, 0};
+// The other waits have 20 ms, so that this one is what ends the kernel.
+__device__ __noinline__ bool hooked_wait(uint64_t* b, uint32_t parity, volatile uint32_t* abort, int which, int at) {
+  uint32_t cluster, rank;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster));
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const bool told = which == g_give_up[0] && int(cluster) == g_give_up[1] && int(rank) == g_give_up[2] && at == g_give_up[3];
+  const uint64_t t0 = global_ns();
+  while (!told) {
+    if (mbar_try_wait(b, parity)) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > 20000000ull) break;
+  }
+  *abort = 1u;
+  atomicExch(&g_gemm_i8_timeout, 1u);
+  return false;
+}
+#endif
+__device__ __forceinline__ bool wait_for(uint64_t* b, uint32_t parity, volatile uint32_t* abort, Wait which, int at) {
+#ifdef WQ_TEST_HOOKS
+  if (g_give_up[0] >= 0) return hooked_wait(b, parity, abort, which, at);
+#endif
   return mbar_try_wait(b, parity) || mbar_wait(b, parity, abort, &g_gemm_i8_timeout);
 }
 // Position in a ring of `stages` slots: the slot and its round's parity, kept by
@@ -279,7 +306,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   if (warp == 0) {
     Slot at;
     for (int i = 0; i < nkb; ++i, at.next(S)) {
-      if (i >= S && !__all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort))) break;
+      if (i >= S && !__all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort, kWaitEmpty, i))) break;
       uint8_t* w = ring + at.s * stage;
       const int k = (kb0 + i) * kBK;
       if (elect_one()) {
@@ -295,7 +322,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     const uint64_t ring_desc = sw128_desc(smem_u32(ring));
     Slot at;
     for (int i = 0; i < nkb; ++i, at.next(S)) {
-      if (!__all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort))) break;
+      if (!__all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort, kWaitFull, i))) break;
       tc_fence_after();
       const uint64_t a = ring_desc + uint32_t(at.s) * (stage >> 4), b = a + (wtile >> 4);
       if (elect_one()) {
@@ -317,7 +344,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
   const float sw = row < p.rows && n < L.N ? (up ? L.s1[n] : L.s0[n]) : 0.0f;
   if (threadIdx.x < mend) xscale[threadIdx.x] = L.xs[m0 + threadIdx.x];
   if (warp < 4) wscale[row] = sw;
-  bool ok = wait_for(&done, 0, abort);
+  bool ok = wait_for(&done, 0, abort, kWaitDone, 0);
   ok = __all_sync(0xffffffffu, ok);   // tcgen05.ld needs the whole warp
   const uint32_t tcol = tmem + (uint32_t(32 * (warp & 3)) << 16);
 
@@ -325,8 +352,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
     // Unsplit: straight from tensor memory, neighbouring lanes to neighbouring
     // outputs.  (Through shared memory, four outputs a thread, 128 tokens of 80
     // rows took 3.8 us for this.)
-    __syncthreads();                    // xscale
-    if (ok) {
+    __syncthreads();                    // xscale; behind it every wait has ended
+    if (!*abort) {                      // else the sums may lack a part of K, though `done` came
       tc_fence_after();
       auto store = [&](auto type) {
         for (int c = 32 * (warp >> 2); c < mend; c += 64) {
@@ -370,8 +397,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const _
         }
       }
     }
-    __syncthreads();
+    __syncthreads();                    // every wait has ended
     if (ks > 1) {
+      // a rank that gave up has not sent (all of) its sums: nobody stores the tile
+      if (*abort && threadIdx.x < uint32_t(ks)) st_cluster(mapa(smem_u32(&abort_word), threadIdx.x), 1u);
+      __syncwarp();
       cluster_arrive();
       cluster_wait();
     }
@@ -562,7 +592,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int mrow = tm * 256 + int(rank) * 128;
       const int nrow = GATED ? tn * out_n : tn * bn + int(rank) * (bn / 2);
       for (int kb = 0; kb < nkb; ++kb, ++issued, at.next(S)) {
-        if (issued >= S) ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort));
+        if (issued >= S)
+          ok = __all_sync(0xffffffffu, wait_for(&empty[at.s], at.parity ^ 1u, abort, kWaitEmpty, int(issued)));
         if (!ok) break;
         uint8_t* a = ring + at.s * stage;
         const uint32_t bar = full0 + uint32_t(at.s) * 8;
@@ -583,12 +614,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       Slot at;
       for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
         const int a = n & 1;
-        if (n >= 2) ok = __all_sync(0xffffffffu, wait_for(&acc_empty[a], ((n >> 1) - 1) & 1, abort));
+        if (n >= 2)
+          ok = __all_sync(0xffffffffu, wait_for(&acc_empty[a], ((n >> 1) - 1) & 1, abort, kWaitAccEmpty, n));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(a) * 256;
         for (int kb = 0; kb < nkb; ++kb, at.next(S)) {
-          ok = __all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort));
+          ok = __all_sync(0xffffffffu, wait_for(&full[at.s], at.parity, abort, kWaitFull, n * nkb + kb));
           if (!ok) break;
           tc_fence_after();
           const uint64_t sa = ring_desc + uint32_t(at.s) * (stage >> 4), sb = sa + (kTile >> 4);
@@ -645,7 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncwarp();
       const float s = sx;
       if (t + step < tiles) load_scales(t + step);
-      ok = wait_for(&acc_full[a], (n >> 1) & 1, abort);
+      ok = wait_for(&acc_full[a], (n >> 1) & 1, abort, kWaitDone, n);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -1010,3 +1042,11 @@ bool gemm_read_and_clear_timeout(cudaError_t* err) {
 
 }  // namespace i8
 }  // namespace wq
+
+#ifdef WQ_TEST_HOOKS
+// Test builds only: which wait of the 8-bit kernels gives up (see g_give_up); 0 on success.
+extern "C" int wq_test_give_up_i8(int which, int cluster, int rank, int at) {
+  const int told[4] = {which, cluster, rank, at};
+  return cudaMemcpyToSymbol(wq::i8::g_give_up, told, sizeof(told)) == cudaSuccess ? 0 : 7;
+}
+#endif
