@@ -112,6 +112,10 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Counts `bytes` as landed on the barrier's present phase.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -534,6 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ uint64_t acc_empty[2];           // leader's: both CTAs' epilogue warps have read it
   __shared__ uint64_t done;                   // all MMAs done (commit to both)
   __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ uint32_t peer_abort, peer_issued[2];     // the other CTA has given up; the stages it had asked for
   // per epilogue warp: the tile's weight scales; 32 rows of 64 output bytes, 16 bytes apart
   __shared__ __align__(16) float wscale_all[8][256];
   __shared__ __align__(16) uint8_t out_all[8][32 * kOutRow];
@@ -561,6 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(&done, 1);
     *abort = 0u;
+    peer_abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -753,22 +759,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  // Given up: the copies in flight land before shared memory goes away.  The
-  // leader's barriers count both CTAs' bytes, but the peer may have asked for
-  // stages that the leader has not come to: it has no barrier to wait on and
-  // lets a time pass that is thousands of times a copy's.
-  if (*abort && warp == 0 && lane == 0) {
-    if (rank == 0) {
-      for (int64_t j = issued > S ? issued - S : 0; j < issued; ++j)
-        mbar_drain(&full[j % S], uint32_t(j / S) & 1u, &g_gemm_i8_timeout);
-    } else {
-      const uint64_t t0 = global_ns();
-      while (global_ns() - t0 < 20000000ull) __nanosleep(1000);
-    }
-  }
+  if (*abort && threadIdx.x == 0) st_cluster(mapa(smem_u32(&peer_abort), rank ^ 1u), 1u);
   if (warp == 1 && lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
   __syncwarp();
-  cluster_sync();           // no arrival or copy of the pair is left in flight
+  cluster_sync();           // no arrival or copy of the pair is left in flight, unless one of the two has given up
+  if (*abort || *static_cast<volatile uint32_t*>(&peer_abort)) {     // the same in both
+    // Given up: the copies in flight land before shared memory goes away.  All of
+    // them complete on the leader's barriers, which count both CTAs' bytes, and
+    // one of the two may have asked for stages that the other has not come to: at
+    // most the ring's last S, as a slot is asked for again only behind the MMAs that
+    // read it.  The leader puts the missing half of these on their barriers and
+    // waits for them; then both go.
+    if (warp == 0 && lane == 0) {
+      const uint32_t at = mapa(smem_u32(peer_issued), rank ^ 1u);
+      st_cluster(at, uint32_t(issued));
+      st_cluster(at + 4, uint32_t(issued >> 32));
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp == 0 && lane == 0 && rank == 0) {
+      const volatile uint32_t* got = peer_issued;
+      const int64_t theirs = int64_t(uint64_t(got[1]) << 32 | got[0]), last = issued > theirs ? issued : theirs;
+      for (int64_t j = last > S ? last - S : 0; j < last; ++j) {
+        uint64_t* bar = &full[j % S];
+        if (j >= issued) mbar_expect_tx(bar, stage);            // the peer's copies alone
+        if (j >= theirs) mbar_complete_tx(bar, stage);          // this CTA's alone
+        mbar_drain(bar, uint32_t(j / S) & 1u, &g_gemm_i8_timeout);
+      }
+    }
+    if (warp == 1 && lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));

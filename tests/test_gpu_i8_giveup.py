@@ -82,7 +82,7 @@ def _run(cases):
     assert len(res) == len(cases)
     for r in res:
         assert r["call"] == 0 and r["error"] == 8 and r["then"] == 0, r
-        assert r["wrong"] == 0 and r["missing"] > 0 and r["after"], r
+        assert r["wrong"] == 0 and r["after"], r
     return res
 
 
@@ -92,5 +92,27 @@ def test_split_kernel_gives_up(name):
     gated, M, N, K = SPLIT[name]
     waits = SPLIT_WAITS + (CLUSTER_WAITS if name.startswith("clusters") else [])
     for r in _run([((gated, M, N, K), w) for w in waits]):
-        assert r["rows"] == M and r["cols"] == r["span"] <= 128 and r["missing"] == M * r["cols"], r
+        assert r["rows"] == M and 0 < r["cols"] == r["span"] <= 128 and r["missing"] == M * r["cols"], r
         assert r["first col"] == 2 * r["cols"], r
+
+
+# three tiles a pair; one
+PAIR = {"three tiles": (False, 520, 18944, 2048), "three tiles gated": (True, 520, 9472, 2048),
+        "one tile": (False, 300, 4096, 4096), "one tile gated": (True, 300, 4096, 4096)}
+# Either CTA's copies stop first, so that the other has some in flight that its peer has not come to; the MMAs stop
+# at the first stage, inside a tile, at a tile's start; an epilogue leaves its first and its last accumulator
+PAIR_WAITS = [(EMPTY, 5, 0, 20), (EMPTY, 5, 1, 20), (EMPTY, 5, 0, 10), (EMPTY, 5, 1, 10), (FULL, 5, 0, 0),
+              (FULL, 5, 0, 13), (DONE, 5, 0, 0), (DONE, 5, 1, 0)]
+TILES_WAITS = [(FULL, 5, 0, 32), (FULL, 5, 0, 47), (ACC_EMPTY, 5, 0, 2), (DONE, 5, 0, 1), (DONE, 5, 1, 2),
+               (EMPTY, 5, 0, 47), (EMPTY, 5, 1, 47)]
+
+
+@pytest.mark.parametrize("name", PAIR)
+def test_pair_kernel_gives_up(name):
+    """Tiles of the one pair are left out, and nothing else; both CTAs' copies have landed when it ends.
+    (Of 300 tokens pair 5 has those from 256 on, and its second CTA, whose rows start at 384, none to leave out.)"""
+    gated, M, N, K = PAIR[name]
+    waits = PAIR_WAITS + (TILES_WAITS if name.startswith("three") else [])
+    for w, r in zip(waits, _run([((gated, M, N, K), w) for w in waits])):
+        assert r["cols"] <= 3 * 256, (w, r)
+        assert (r["missing"] > 0) == (M > 384 or w != (DONE, 5, 1, 0)), (w, r)
