@@ -276,9 +276,14 @@ typedef enum {
  * wq_quantize_i8 -- every row of x to 8-bit codes with a scale of its own.
  *
  *   s = max_k |x_k| * fp32(1/127) in fp32,  q_k = rint(x_k / s)  (of the exact
- *   quotient, half to even, kept within -127..127); s = 0 and q = 0 for a row of zeros;
- *   s = NaN and q = 0 for a row that holds an infinity or a NaN, so that
- *   every product with that row is NaN
+ *   quotient, half to even, kept within -127..127); s = 0 and q = 0 for a row of zeros
+ *   and one of magnitudes up to 63 * 2^-149, whose s is rounded to 0; s = NaN and
+ *   q = 0 for a row that holds an infinity or a NaN, so that every product with
+ *   that row is NaN
+ *
+ * s is this one product, not max_k |x_k| / 127 rounded once: the two differ in the
+ * last place for about one row in twenty (s is off max_k |x_k| / 127 by up to 6.3e-8
+ * of it, the rounded quotient by 6.0e-8), and with them codes next to a half.
  *
  *   x        in   x_type [R, K], row stride ldx: tokens, or rows of weights
  *   codes    out  int8 [R, K], row stride ldc (16-byte aligned, ldc % 16 == 0)

@@ -6,6 +6,8 @@
 //
 //   s = max |x| fp32(1 / 127),   q = clamp(rint(x / s), -127, 127),  0 where s = 0
 //
+// (s one product and one rounding; the rounded quotient max |x| / 127 is its
+// neighbour for one row in twenty, and other codes next to a half go with it)
 // with rint of the exact quotient, half to even; a row that holds an infinity
 // or a NaN gets s = NaN and q = 0, so that every product with it is NaN.
 //
