@@ -306,8 +306,9 @@ wq_status wq_quantize_i8(const void* x, wq_type x_type, int64_t R, int64_t K, in
  * does not depend on M, on the other rows or on which kernel ran, bit for bit.
  * A NaN scale gives a row or column of NaNs, an infinite one infinities (NaN
  * where the sum is 0).  M <= 8 runs on warp-level MMAs, larger batches on
- * tcgen05: weights on the MMA's M side and K split over a cluster up to 128
- * rows, pairs of SMs on 256-row tiles above.
+ * tcgen05: up to 128 rows, and above where few outputs and long sums would leave
+ * most SMs without a tile, weights on the MMA's M side and K split over a cluster;
+ * else pairs of SMs on 256-row tiles.
  */
 wq_status wq_gemm_i8(const int8_t* x, int64_t ldx, const float* x_scales, int64_t M, int64_t N, int64_t K,
                      const int8_t* w, int64_t ldw, const float* w_scales, void* y, wq_type y_type, int64_t ldy,
