@@ -799,16 +799,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------ host
 
-int sm_count(int dev) {
-  static std::atomic<int> cached[64];
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) n = 2;
-    cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 // Largest dynamic shared memory, once per kernel and device.
 template <typename F>
 cudaError_t allow_smem(F* fn, uint32_t bytes, std::atomic<bool>* set, int dev) {
@@ -823,12 +813,6 @@ cudaError_t allow_smem(F* fn, uint32_t bytes, std::atomic<bool>* set, int dev) {
 bool make_map(CUtensorMap* map, const int8_t* base, int64_t K, int64_t rows, int64_t ld, int box_rows) {
   return make_tensor_map_2d(map, TmaType::kU8, base, uint64_t(K), uint64_t(rows), uint64_t(ld), kBK,
                             uint32_t(box_rows), 128);
-}
-
-cudaError_t current_device(int* dev) {
-  const cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return e;
-  return *dev >= 0 && *dev < 64 ? cudaSuccess : cudaErrorInvalidDevice;
 }
 
 template <int ACT>
@@ -1038,6 +1022,22 @@ cudaError_t launch_as(const Linear& L, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t current_device(int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return *dev >= 0 && *dev < 64 ? cudaSuccess : cudaErrorInvalidDevice;
+}
+
+int sm_count(int dev) {
+  static std::atomic<int> cached[64];
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) n = 2;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 cudaError_t launch_linear(const Linear& L, cudaStream_t st) {
   if (L.M <= kGemvTokens) return launch_gemv(L, st);

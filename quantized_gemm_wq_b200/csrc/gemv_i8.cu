@@ -183,9 +183,12 @@ template <bool GATED, int U>
 cudaError_t launch_as(const Linear& L, cudaStream_t st) {
   const int64_t tiles = (L.N + 15) / 16;
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  int dev;
+  const cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
   // Eight warps a CTA; sixteen where there are fewer tiles than SMs (1024 rows,
   // K = 8192: 4.2 against 5.6 us; 11008 rows, K = 4096: 14.0 against 10.1).
-  const int warps = tiles < 148 ? 16 : 8;
+  const int warps = tiles < sm_count(dev) ? 16 : 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles));
   cfg.blockDim = dim3(unsigned(32 * warps));

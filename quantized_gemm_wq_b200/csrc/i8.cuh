@@ -131,6 +131,10 @@ __device__ __forceinline__ void store_one(void* y, int64_t i, float v, int type)
 __device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The current device (of up to 64), and its SMs.
+cudaError_t current_device(int* dev);
+int sm_count(int dev);
+
 cudaError_t launch_quantize(const void* x, int type, int64_t R, int64_t K, int64_t ldx, int8_t* codes,
                             int64_t ldc, float* scales, cudaStream_t st);
 // Up to kGemvTokens tokens.

@@ -261,12 +261,16 @@ cudaError_t launch_typed(const void* x, int64_t R, int64_t K, int64_t ldx, int8_
                          cudaStream_t st) {
   constexpr int VE = Vec<TYPE>::VE;
   const int64_t nvec = K / VE;
+  int dev;
+  const cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t busy = 16 * sm_count(dev);     // warps
   // Warps per row: what a thread does once per row (the maxima's exchange, the
   // scale) costs as much as 20 elements, so up to eight vectors a thread; fewer
   // where the rows alone do not give every SM 16 warps.  Rows that eight warps
   // cannot hold go to CTAs of sixteen.
   int lw = 0;
-  while (lw < 3 && (nvec > (256 << lw) || (nvec > (32 << lw) && (R << lw) < 148 * 16))) ++lw;
+  while (lw < 3 && (nvec > (256 << lw) || (nvec > (32 << lw) && (R << lw) < busy))) ++lw;
   if (nvec > 2048) lw = 4;
   const int64_t per = (nvec + (32 << lw) - 1) / (32 << lw);
   const int warps = lw == 4 ? 16 : 8;
