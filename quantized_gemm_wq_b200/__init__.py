@@ -317,7 +317,7 @@ def _output(y, M: int, N: int, dtype, x):
 
 
 def wq_quantize_i8(x: torch.Tensor, codes=None, scales=None, stream=None):
-    """Quantise every row of bf16/fp16/fp32 ``x`` [R, K] (CUDA, any row stride)
+    """Quantise every row of bf16/fp16/fp32 ``x`` [R, K] (CUDA, any row stride from K on)
     -> (int8 codes [R, K], fp32 scales [R]), ``x ~ codes * scales[:, None]``;
     a row's scale is max|x| times fp32(1/127).
     The codes' rows start at multiples of 32 bytes, so for other K they do not

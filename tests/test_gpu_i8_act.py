@@ -108,3 +108,18 @@ def test_activation_error(act, dtype, M):
     ref, v = _reference(g, act)
     err = np.abs(ref) * _units(g, v, act, dtype) * U * 1.01 + 2.0 ** -140
     assert_rounds_to(_act(g, act, M, dtype)[M - 1:], ref[None], err[None], f"{act} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_gates_at_the_ends(act, dtype, M):
+    """Gates whose square or cube leaves fp32, infinite ones and NaN: the limit above zero and below,
+    NaN for minus infinity (a product of it and 0) and for NaN."""
+    inf = float("inf")
+    g = np.array([3e19, 3e38, inf, -3e19, -3e38, -200.0, -inf, np.nan, 0.0, -0.0], np.float32)
+    h = _act(g, act, M, dtype)[M - 1]
+    top = torch.from_numpy(g[:3]).to(dtype).cuda()
+    assert torch.equal(h[:3], top)
+    assert (h[3:6] == 0).all() and torch.isnan(h[6:8]).all()
+    assert (h[8:] == 0).all() and torch.signbit(h[8:]).tolist() == [False, True]
