@@ -314,12 +314,12 @@ __device__ __forceinline__ void sw_tile(const CUtensorMap* tm_x, const CUtensorM
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ep_ok = false;
+  int issued = 0;                      // copies that a producer has asked for
 
   if (warp == 0) {
     // ------------------------------------------------------------ code producer
     if (lane == 0) {
       const int nc = (kt1 - kt0 + 1) / 2;              // 128-wide code stages of this split
-      int issued = 0;
       bool ok = true;
       for (int c = 0; c < nc && ok; ++c) {
         const int cs = c % SC;
@@ -329,13 +329,10 @@ __device__ __forceinline__ void sw_tile(const CUtensorMap* tm_x, const CUtensorM
         tma_load_2d(sC + cs * Cfg::kCBytes, tm_c, &full_c[cs], ((kt0 >> 1) + c) * (CK * BITS / 32), int(n0));
         ++issued;
       }
-      if (!ok)   // copies in flight land before shared memory goes away
-        for (int c = (issued > SC ? issued - SC : 0); c < issued; ++c) mbar_drain(&full_c[c % SC], (c / SC) & 1);
     }
   } else if (warp == kXWarp) {
     // ------------------------------------------------------------ x producer
     if (lane == 0) {
-      int issued = 0;
       bool ok = true;
       for (int kt = kt0; kt < kt1 && ok; ++kt) {
         const int j = kt - kt0, s = j % SX;
@@ -345,8 +342,6 @@ __device__ __forceinline__ void sw_tile(const CUtensorMap* tm_x, const CUtensorM
         tma_load_2d(sX + s * Cfg::kXBytes, tm_x, &full_x[s], kt * BK, 0);
         ++issued;
       }
-      if (!ok)
-        for (int j = (issued > SX ? issued - SX : 0); j < issued; ++j) mbar_drain(&full_x[j % SX], (j / SX) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -546,6 +541,15 @@ __device__ __forceinline__ void sw_tile(const CUtensorMap* tm_x, const CUtensorM
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
+  // Given up, by whichever warp: copies in flight land before shared memory goes
+  // away (the producers may have asked for their last ones long ago).
+  if (*abort && lane == 0) {
+    if (warp == 0)
+      for (int c = (issued > SC ? issued - SC : 0); c < issued; ++c) mbar_drain(&full_c[c % SC], (c / SC) & 1);
+    if (warp == kXWarp)
+      for (int j = (issued > SX ? issued - SX : 0); j < issued; ++j) mbar_drain(&full_x[j % SX], (j / SX) & 1);
+  }
+  __syncwarp();
   if (warp == 1) {
     if (*abort) {
       if (lane == 0) mbar_drain(tmem_full, 0);       // MMAs issued finish before tensor memory is freed

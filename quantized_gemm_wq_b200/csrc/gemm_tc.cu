@@ -317,6 +317,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ep_ok = false;                         // dequant warps: accumulators are final
+  int issued_a = 0, issued_c = 0;             // copies that the producer has asked for
   // A second launch of this kernel over other tiles of the same y (the
   // leftover tiles of a two-launch plan) may take SMs as this one frees them.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -324,7 +325,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int issued_a = 0, issued_c = 0;
       bool ok = true;
       for (int kt = kt0; kt < kt1 && ok; ++kt) {
         const int j = kt - kt0;                         // local step (ring phase)
@@ -342,12 +342,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         mbar_expect_tx(&full_a[s], kABytes);
         tma_load_2d(sA + s * kABytes, &tm_x, &full_a[s], kt * BK, int(m0));
         ++issued_a;
-      }
-      if (!ok) {   // let the copies still in flight land before shared memory goes away
-        for (int kt = (issued_a > SX ? issued_a - SX : 0); kt < issued_a; ++kt)
-          mbar_drain(&full_a[kt % SX], (kt / SX) & 1);
-        for (int c = (issued_c > SC ? issued_c - SC : 0); c < issued_c; ++c)
-          mbar_drain(&full_c[c % SC], (c / SC) & 1);
       }
     }
   } else if (warp == 1) {
@@ -590,6 +584,13 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
+  // Given up, by whichever warp: copies in flight land before shared memory goes
+  // away (the producer may have asked for its last ones long ago).
+  if (*abort && warp == 0 && lane == 0) {
+    for (int j = (issued_a > SX ? issued_a - SX : 0); j < issued_a; ++j) mbar_drain(&full_a[j % SX], (j / SX) & 1);
+    for (int c = (issued_c > SC ? issued_c - SC : 0); c < issued_c; ++c) mbar_drain(&full_c[c % SC], (c / SC) & 1);
+  }
+  __syncwarp();
   if (warp == 1) {
     if (*abort) {
       if (lane == 0) mbar_drain(tmem_full, 0);   // MMAs issued must finish before TMEM is freed

@@ -195,11 +195,11 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __nv_bfloat16* __
   for (int m = 0; m < MP; ++m) acc[m] = 0.0f;
   const int dw = warp - 2, q = warp & 3, h = dw >> 2;
   const int row = 32 * q + lane;
+  int ic = 0;                          // copies that the producer has asked for
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int ic = 0;
       bool ok = true;
       for (int j = 0; j < J && ok; ++j) {
         const int cs = j % RC;
@@ -209,8 +209,6 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __nv_bfloat16* __
         tma_load_2d(sC + cs * C::kBox, &tm_c, &c_full[cs], (s0 + j) * C::kWords, int(n0));
         ++ic;
       }
-      if (!ok)   // copies in flight must land before shared memory goes away
-        for (int j = (ic > RC ? ic - RC : 0); j < ic; ++j) mbar_drain(&c_full[j % RC], (j / RC) & 1, flag);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
@@ -447,6 +445,11 @@ gemv_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __nv_bfloat16* __
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
+  // Given up, by whichever warp: copies in flight land before shared memory goes
+  // away (the producer may have asked for its last ones long ago).
+  if (*abort && warp == 0 && lane == 0)
+    for (int j = (ic > RC ? ic - RC : 0); j < ic; ++j) mbar_drain(&c_full[j % RC], (j / RC) & 1, flag);
+  __syncwarp();
   if (warp == 1) {
     if (lane == 0) mbar_drain(mma_done, 0, flag);     // issued MMAs finish before TMEM is freed
     __syncwarp();
