@@ -251,6 +251,13 @@ constexpr int kSplitRowsMin = 64;
 // the idle rows the MMA reads on into what follows, this far at most.
 constexpr uint32_t kSplitSlack = (128 - kSplitRowsMin) * kBK;
 
+// Tensor memory is allocated without a limit on the wait, and a cluster or a
+// dependent kernel may wait for a CTA that waits for it: so CTAs that share an SM
+// by their shared memory have to fit its 512 columns.  Two of this kernel do (at
+// most 128 columns and at least 75 KB each), beside each other or a CTA of the
+// weight-only kernels that run two an SM (256 columns, 100 KB); beside the kernels
+// that take all 512 (the pair kernel, 197 KB, and the prefill GEMM) none has room.
+
 template <int ACT>
 __global__ void __launch_bounds__(kSplitThreads, 2) gemm_i8_split_kernel(const __grid_constant__ SplitArgs p) {
   constexpr bool GATED = ACT != kNone;
@@ -526,6 +533,37 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm
   tn = r / rows;
 }
 
+// What is left to wait for when a CTA of the pair has given up: both call this.  The
+// copies in flight have to land before shared memory goes away.  All of them complete
+// on the leader's barriers, which count both CTAs' bytes, and one of the two may have
+// asked for stages that the other has not come to: at most the ring's last S, as a
+// slot is asked for again only behind the MMAs that read it.  The leader puts the
+// missing half of these on their barriers and waits for them; then both go.
+// (Its own function: inline it cost every call 0.1 us at the kernel's end.)
+__device__ __noinline__ void pair_gave_up(uint64_t* full, uint64_t* done, uint32_t* peer_issued, int64_t issued, int S,
+                                          uint32_t stage, uint32_t rank) {
+  if (threadIdx.x == 0) {               // of the producer warp
+    const uint32_t at = mapa(smem_u32(peer_issued), rank ^ 1u);
+    st_cluster(at, uint32_t(issued));
+    st_cluster(at + 4, uint32_t(issued >> 32));
+  }
+  __syncwarp();
+  cluster_sync();
+  if (threadIdx.x == 0 && rank == 0) {
+    const volatile uint32_t* got = peer_issued;
+    const int64_t theirs = int64_t(uint64_t(got[1]) << 32 | got[0]), last = issued > theirs ? issued : theirs;
+    for (int64_t j = last > S ? last - S : 0; j < last; ++j) {
+      uint64_t* bar = &full[j % S];
+      if (j >= issued) mbar_expect_tx(bar, stage);            // the peer's copies alone
+      if (j >= theirs) mbar_complete_tx(bar, stage);          // this CTA's alone
+      mbar_drain(bar, uint32_t(j / S) & 1u, &g_gemm_i8_timeout);
+    }
+  }
+  if (threadIdx.x == 32) mbar_drain(done, 0, &g_gemm_i8_timeout);
+  __syncwarp();
+  cluster_sync();
+}
+
 template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_i8_pair_kernel(const __grid_constant__ PairArgs p) {
@@ -763,34 +801,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 1 && lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
   __syncwarp();
   cluster_sync();           // no arrival or copy of the pair is left in flight, unless one of the two has given up
-  if (*abort || *static_cast<volatile uint32_t*>(&peer_abort)) {     // the same in both
-    // Given up: the copies in flight land before shared memory goes away.  All of
-    // them complete on the leader's barriers, which count both CTAs' bytes, and
-    // one of the two may have asked for stages that the other has not come to: at
-    // most the ring's last S, as a slot is asked for again only behind the MMAs that
-    // read it.  The leader puts the missing half of these on their barriers and
-    // waits for them; then both go.
-    if (warp == 0 && lane == 0) {
-      const uint32_t at = mapa(smem_u32(peer_issued), rank ^ 1u);
-      st_cluster(at, uint32_t(issued));
-      st_cluster(at + 4, uint32_t(issued >> 32));
-    }
-    __syncwarp();
-    cluster_sync();
-    if (warp == 0 && lane == 0 && rank == 0) {
-      const volatile uint32_t* got = peer_issued;
-      const int64_t theirs = int64_t(uint64_t(got[1]) << 32 | got[0]), last = issued > theirs ? issued : theirs;
-      for (int64_t j = last > S ? last - S : 0; j < last; ++j) {
-        uint64_t* bar = &full[j % S];
-        if (j >= issued) mbar_expect_tx(bar, stage);            // the peer's copies alone
-        if (j >= theirs) mbar_complete_tx(bar, stage);          // this CTA's alone
-        mbar_drain(bar, uint32_t(j / S) & 1u, &g_gemm_i8_timeout);
-      }
-    }
-    if (warp == 1 && lane == 0) mbar_drain(&done, 0, &g_gemm_i8_timeout);
-    __syncwarp();
-    cluster_sync();
-  }
+  if ((*abort | *static_cast<volatile uint32_t*>(&peer_abort)) != 0u)      // the same in both
+    pair_gave_up(full, &done, peer_issued, issued, S, stage, rank);
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
